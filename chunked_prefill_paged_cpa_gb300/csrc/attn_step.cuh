@@ -56,7 +56,21 @@
 // v_scale into the output.  The widening also zeroes the rows of cache slots
 // past the sequence.
 //
-// This header is compiled once per cache mode (attn_step_<mode>.cu).
+// Sliding window with sinks (template WIN): the row at position x sees the keys
+// j <= x with j < sinks or j > x - window.  The rows of one item between them
+// see the pages of the sinks and the pages from the first row's window to the
+// last row, two runs of the block table.  The item's keys are numbered through
+// both runs ("virtual" positions: the pages behind the sinks moved down by the
+// length of the gap, a whole number of pages), so that the tiles, splits,
+// slices and merges are those of a shorter sequence: only the producer's look-up
+// of a page adds the gap again.  In virtual positions a row at x still sees
+// v <= x and (v < sinks or v > x - window); the tiles that hold an edge of the
+// window are masked like those of the diagonal.  A step then costs what its
+// visible keys cost, whatever the length of the sequences: pages outside are
+// neither read nor looked up (their entries may be anything, freed pages say).
+//
+// This header is compiled once per cache mode (attn_step_<mode>.cu), and once
+// more with the window (attn_window_<mode>.cu).
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -172,6 +186,27 @@ __device__ __forceinline__ int tile_kv(int ctx, int q_len, int m) {
   return (ctx - q_len + min(m * TM + TM - 1, q_len - 1)) / BN + 1;
 }
 
+// Pages that an item leaves out between the sinks and its first row's window
+// (its first row at position x): virtual page v is page v + gap behind the sinks.
+template <bool WIN>
+__device__ __forceinline__ int gap_pages(const AttnParams &p, int x) {
+  if (!WIN) return 0;
+  return max(0, max(0, x - p.window + 1) / kPage - ceil_div(p.sinks, kPage));
+}
+
+// Context of a decode in virtual positions.
+template <bool WIN>
+__device__ __forceinline__ int decode_ctx(const AttnParams &p, int ctx) {
+  return ctx - kPage * gap_pages<WIN>(p, ctx - 1);
+}
+
+// KV tiles of tile pair mp of a chunk (mt query tiles).
+template <int G, bool WIN>
+__device__ __forceinline__ int pair_kv(const AttnParams &p, int ctx, int q_len, int mp, int mt) {
+  const int gap = gap_pages<WIN>(p, ctx - q_len + 2 * mp * (BM / G));
+  return tile_kv<G>(ctx - kPage * gap, q_len, min(2 * mp + 1, mt - 1));
+}
+
 // Queue entry written by the plan kernel (32 bytes, two 16-byte stores).
 struct __align__(16) ItemDesc {
   int s_kind;   // sequence | KIND_DECODE << 30
@@ -201,7 +236,7 @@ __host__ __device__ __forceinline__ int64_t plan_q_pieces(const AttnParams &p) {
   return (KVM == 2 && !p.act_f16) ? (int64_t)p.num_tokens * p.Hq * (p.D * 2 / 16) : 0;
 }
 
-template <int KVM, int G>
+template <int KVM, int G, bool WIN>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p,
                                                                   const StepWs w) {
   // the step kernel may be scheduled now: it waits in grid_dependency_wait
@@ -287,12 +322,19 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     sq_len[s] = q_len;
     sq_ctx[s] = ctx;
     if (q_len == 1) {
-      pages += (long long)Hkv * ceil_div(ctx, kPage);
+      pages += (long long)Hkv * ceil_div(decode_ctx<WIN>(p, ctx), kPage);
     } else if (q_len > 1) {
       const int mt = ceil_div(q_len * G, BM), npair = (mt + 1) / 2;
       pairs += (long long)Hkv * npair;
-      // tiles per pair grow about linearly from the first pair to the last
-      ctiles += (long long)Hkv * npair * (tile_kv<G>(ctx, q_len, 1) + tile_kv<G>(ctx, q_len, mt - 1)) / 2;
+      // tiles per pair grow about linearly from the first pair to the last, or
+      // until they fill the window: one more sample, in the middle
+      const int t0 = pair_kv<G, WIN>(p, ctx, q_len, 0, mt);
+      const int t1 = pair_kv<G, WIN>(p, ctx, q_len, npair - 1, mt);
+      if (WIN)
+        ctiles += (long long)Hkv * npair *
+                  (t0 + 2 * pair_kv<G, WIN>(p, ctx, q_len, npair / 2, mt) + t1) / 4;
+      else
+        ctiles += (long long)Hkv * npair * (t0 + t1) / 2;
     }
   }
 #pragma unroll
@@ -325,11 +367,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
       (int)max((long long)kMinUnitTiles, ((tt + (tp + 7) / 8 + grid - 1) / grid * 3 + 3) / 4);
   auto units = [&](int s) {  // chunk units of one kv head of sequence s
     const int mt = ceil_div(sq_len[s] * G, BM), npair = (mt + 1) / 2;
-    return npair * min(nu, ceil_div(tile_kv<G>(sq_ctx[s], sq_len[s], mt - 1), unit_tiles));
+    return npair * min(nu, ceil_div(pair_kv<G, WIN>(p, sq_ctx[s], sq_len[s], npair - 1, mt), unit_tiles));
   };
-  auto pieces = [&](int s) { return ceil_div(ceil_div(sq_ctx[s], kPage), P); };
+  auto dec_pages = [&](int s) { return ceil_div(decode_ctx<WIN>(p, sq_ctx[s]), kPage); };
+  auto pieces = [&](int s) { return ceil_div(dec_pages(s), P); };
   auto bucket = [&](int s) {  // size class of a decode sequence's pieces, in blocks
-    const int n = ceil_div(sq_ctx[s], kPage);
+    const int n = dec_pages(s);
     return min(ceil_div(ceil_div(n, pieces(s)), 8), kSizeBuckets - 1);
   };
 
@@ -426,7 +469,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   }
   for (int i = tid; i < Nd; i += kPlanWorkers) {
     const int s = search(s_dec, i);
-    const int n = ceil_div(sq_ctx[s], kPage), ks = pieces(s);
+    const int n = dec_pages(s), ks = pieces(s);
     const int local = i - s_dec[s];
     const int g = local / ks, piece = local - g * ks;
     ItemDesc d;
@@ -467,6 +510,18 @@ __device__ __forceinline__ void mask_chunk(uint32_t (&sr)[32], int n) {
     if (e >= n) sr[e] = __float_as_uint(-INFINITY);
 }
 
+// The same with a window: of a 32-column chunk the keys before n stay that lie
+// before a (the sinks) or from b on.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+__device__ __forceinline__ void mask_window(uint32_t (&sr)[32], int n, int a, int b) {
+  const uint32_t keep = low_bits(n) & (low_bits(a) | ~low_bits(b));
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(keep >> e & 1u)) sr[e] = __float_as_uint(-INFINITY);
+}
+
 // p = exp2(s * scale - m) for 32 columns as 16 bf16 (F16: binary16) pairs in
 // `pw`; the fp32 row sum (packed pairs) goes to four independent accumulators.
 template <bool F16>
@@ -499,14 +554,15 @@ __device__ __forceinline__ uint16_t cvt_out(float a, bool f16) {
 // One page of E4M3 codes (16 rows x D bytes at `src`, row-major) widened to
 // binary16 in the 128-byte-swizzled layout the MMAs read: row rr of panel p at
 // dst + p * pstride + rr * 128, its 16-byte chunk c at position c ^ (rr & 7).
-// Rows >= zrow (cache slots past the sequence) become zeros.  The codes lie
+// Rows >= zrow (cache slots past the sequence) become zeros, and with a window
+// rows z0 .. z1 - 1 (keys that no row of the item sees).  The codes lie
 // inside the page's own destination (the last panel's rows at D = 128, the
 // second half of the rows at D = 64): taken a group of rows at a time, in
 // order, a group's stores land only on its own codes (read before the
 // __syncwarp) or on those of groups already done.
-template <int D>
+template <int D, bool WIN>
 __device__ __forceinline__ void widen_page(const unsigned char *src, unsigned char *dst,
-                                           int pstride, int zrow, int lane) {
+                                           int pstride, int zrow, int z0, int z1, int lane) {
   constexpr int CPR = D / 16;       // 16-byte chunks of codes per row
   constexpr int N = 16 * CPR / 32;  // groups of 32 / CPR rows: 4 (D = 128) or 2 (D = 64)
 #pragma unroll
@@ -519,7 +575,7 @@ __device__ __forceinline__ void widen_page(const unsigned char *src, unsigned ch
     ptx::e4m3x4_to_f16x4(in.y, w[2], w[3]);
     ptx::e4m3x4_to_f16x4(in.z, w[4], w[5]);
     ptx::e4m3x4_to_f16x4(in.w, w[6], w[7]);
-    if (rr >= zrow) {
+    if (rr >= zrow || (WIN && rr >= z0 && rr < z1)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 0u;
     }
@@ -545,15 +601,19 @@ __device__ __forceinline__ void fill_of(int f, int n, bool &is_v, int &t) {
 }
 
 // Derive an item's geometry from its queue entry (every lane computes the same).
-template <int D, int G>
-__device__ __forceinline__ void derive_item(const AttnParams &p, const ItemDesc &d, WorkItem &it) {
+// Returns the pages left out behind the sinks; the item's positions are virtual.
+template <int D, int G, bool WIN>
+__device__ __forceinline__ int derive_item(const AttnParams &p, const ItemDesc &d, WorkItem &it) {
   constexpr int TM = BM / G;
+  const bool dec = (d.s_kind >> 30) == KIND_DECODE;
+  const int gap = gap_pages<WIN>(p, dec ? d.ctx - 1 : d.ctx - d.q_len + 2 * (d.g_x >> 8) * TM);
+  const int ctx = d.ctx - kPage * gap;
   it.s = d.s_kind & 0x3fffffff;
   it.qs = d.qs;
-  it.ctx = d.ctx;
+  it.ctx = ctx;
   it.g = d.g_x & 0xff;
-  it.n_pages = ceil_div(d.ctx, kPage);
-  if ((d.s_kind >> 30) == KIND_DECODE) {
+  it.n_pages = ceil_div(ctx, kPage);
+  if (dec) {
     it.kind = KIND_DECODE;
     it.q_len = 1;
     it.nsplit = d.q_len;
@@ -574,8 +634,8 @@ __device__ __forceinline__ void derive_item(const AttnParams &p, const ItemDesc 
     const int u = d.a & 0xffff, nu = d.a >> 16;
     const int mt = ceil_div(d.q_len * G, BM);
     const int m0 = 2 * it.mp, m1 = m0 + 1;
-    it.n_kv[0] = tile_kv<G>(d.ctx, d.q_len, m0);
-    it.n_kv[1] = m1 < mt ? tile_kv<G>(d.ctx, d.q_len, m1) : 0;
+    it.n_kv[0] = tile_kv<G>(ctx, d.q_len, m0);
+    it.n_kv[1] = m1 < mt ? tile_kv<G>(ctx, d.q_len, m1) : 0;
     const int nkv = max(it.n_kv[0], it.n_kv[1]);
     it.n_kv_max = nkv;
     const int j0 = u * nkv / nu, j1 = (u + 1) * nkv / nu;
@@ -588,8 +648,8 @@ __device__ __forceinline__ void derive_item(const AttnParams &p, const ItemDesc 
     it.nsplit = nu;
     it.slot = d.b;
     it.first_slot = d.c;
-    (void)TM;
   }
+  return gap;
 }
 
 // Warpgroup-wide sync on an mbarrier of 128 arrivals (bounded).
@@ -634,7 +694,7 @@ struct VRing {
   }
 };
 
-template <int KVM, int D, int G>
+template <int KVM, int D, int G, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_qd, const __grid_constant__ CUtensorMap tm_k,
@@ -744,8 +804,9 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
     }
     for (;;) {
       WorkItem it;
+      int gap = 0;
       if (have) {
-        derive_item<D, G>(p, dsc, it);
+        gap = derive_item<D, G, WIN>(p, dsc, it);
         if (it.n_tiles == 0) {  // a unit with no keys in its range
           have = fetch(claim(), dsc);
           continue;
@@ -802,10 +863,11 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       // holds page wb + 32 b + l of window b), the next window prefetched
       const int32_t *bt = p.block_table + (int64_t)it.s * p.max_pages;
       const int wb = it.page0 + 8 * it.j0;
+      const int sink_pages = WIN ? ceil_div(p.sinks, kPage) : 0;
       auto load_window = [&](int b) -> int {
         const int pi = wb + 32 * b + lane;
         if (pi >= it.page_end) return kv_rows;  // past the item: zero fill
-        const int page = __ldg(bt + pi);
+        const int page = __ldg(bt + (WIN && pi >= sink_pages ? pi + gap : pi));
         if (page < 0 || page >= p.num_pages) {
           atomicOr(p.status, STATUS_BAD_PAGE);
           return kv_rows;
@@ -1205,6 +1267,11 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       if (it.kind == KIND_DONE) break;
       const int n_mine = (ti ? it.n_mine[1] : it.n_mine[0]);
       const int ctx = it.ctx;
+      // With a window: keys z0 .. z1 - 1 lie behind the sinks and before the
+      // window of the item's first row, in the pages that hold those edges.  No
+      // row sees them; their V rows are zeroed, since 0 * NaN is NaN inside PV.
+      const int z0 = WIN ? p.sinks : 0;
+      const int z1 = WIN ? (it.kind == KIND_CHUNK ? ctx - it.q_len + 2 * it.mp * TM : ctx - 1) - p.window + 1 : 0;
       vr.begin(it.kind);
       // E4M3 cache: widen the item's fills, in the producer's order, up to
       // fill `last` (this warp: page `warp` of each tile).  Every softmax warp
@@ -1235,11 +1302,11 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           if (!__all_sync(0xffffffffu, ptx::mbar_wait(full, par))) return false;
           const int key0 = (it.page0 + 8 * (it.j0 + t) + warp) * kPage;  // this page's first key
           if (is_v)
-            widen_page<D>(stage + warp * C::PAGE_BYTES + C::V8_OFF, stage + warp * C::PAGE_BYTES,
-                          kPage * 128, ctx - key0, lane);
+            widen_page<D, WIN>(stage + warp * C::PAGE_BYTES + C::V8_OFF, stage + warp * C::PAGE_BYTES,
+                               kPage * 128, ctx - key0, z0 - key0, z1 - key0, lane);
           else
-            widen_page<D>(stage + warp * kPage * 128 + C::K8_OFF, stage + warp * kPage * 128,
-                          BN * 128, ctx - key0, lane);
+            widen_page<D, WIN>(stage + warp * kPage * 128 + C::K8_OFF, stage + warp * kPage * 128,
+                               BN * 128, ctx - key0, z0 - key0, z1 - key0, lane);
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(conv);
         }
@@ -1259,13 +1326,24 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           const int key0 = (it.j0 + j) * BN;
           const bool diag = key0 + BN - 1 > last;  // tile holds keys past `last`
           const int nvis = last - key0 + 1;        // visible keys of this row in the tile
+          // with a window: the row's sinks end, and its window begins, at
+          // these columns of the tile
+          const int wa = WIN ? p.sinks - key0 : 0, wb = WIN ? last - p.window + 1 - key0 : 0;
+          const bool edge = WIN && wb > 0 && wa < BN;
+          auto mask = [&](uint32_t (&x)[32], int c0) {
+            if (WIN) {
+              if (diag || edge) mask_window(x, nvis - c0, wa - c0, wb - c0);
+            } else if (diag) {
+              mask_chunk(x, nvis - c0);
+            }
+          };
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t sa[32];
             ptx::tmem_ld32(tS + c * 32, sa);
             ptx::tmem_wait_ld_regs(sa);
-            if (diag) mask_chunk(sa, nvis - c * 32);
+            mask(sa, c * 32);
 #pragma unroll
             for (int h = 0; h < 16; ++h)
               mx[h & 3] = ptx::max3(mx[h & 3], __uint_as_float(sa[2 * h]), __uint_as_float(sa[2 * h + 1]));
@@ -1296,11 +1374,11 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
             ptx::tmem_ld32(tS + c * 32, sa);
             ptx::tmem_ld32(tS + (c + 1) * 32, sb);
             ptx::tmem_wait_ld_regs(sa);
-            if (diag) mask_chunk(sa, nvis - c * 32);
+            mask(sa, c * 32);
             exp_chunk_regs<F16>(sa, sc2, nm2, rs2, w16);
             ptx::tmem_st16(tS + c * 16, w16);
             ptx::tmem_wait_ld_regs(sb);
-            if (diag) mask_chunk(sb, nvis - (c + 1) * 32);
+            mask(sb, (c + 1) * 32);
             exp_chunk_regs<F16>(sb, sc2, nm2, rs2, w16);
             ptx::tmem_st16(tS + (c + 1) * 16, w16);
           }
@@ -1313,13 +1391,14 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           // Cache slots at or past ctx in the last page may hold anything (NaN
           // included) and 0 * NaN is NaN inside PV: zero those V rows first
           // (an E4M3 cache: already zeroed by the widening).
-          if (KVM != 2 && key0 + BN > ctx) {
+          if (KVM != 2 && (key0 + BN > ctx || (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
             const int vst = vr.stage(j);
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bs->v_full[vst], vr.use(j) & 1))) {
               ok = false;
               break;
             }
-            if (r >= ctx - key0 && r < it.n_pages * kPage - key0) {
+            if ((r >= ctx - key0 && r < it.n_pages * kPage - key0) ||
+                (WIN && r >= z0 - key0 && r < z1 - key0)) {
               unsigned char *vrow = v_stage(vst) + (r / kPage) * C::PAGE_BYTES + (r % kPage) * 128;
 #pragma unroll
               for (int pl = 0; pl < C::PANELS; ++pl)
@@ -1464,7 +1543,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           uint32_t sr[G];
           ptx::tmem_ld_cols<G>(tS, sr);
           const int key = (it.page0 + 8 * blk) * kPage + r;
-          const bool valid = key < key_lim;
+          const bool valid = key < key_lim && (!WIN || key < z0 || key >= z1);
           float sv[G];
 #pragma unroll
           for (int q = 0; q < G; ++q) {
@@ -1506,13 +1585,15 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           // cache slots past ctx in the sequence's last page: zero their V rows
           // (an E4M3 cache: already zeroed by the widening)
           const int key0 = (it.page0 + 8 * blk) * kPage;
-          if (KVM != 2 && key0 + BN > ctx && key0 < it.n_pages * kPage) {
+          if (KVM != 2 && ((key0 + BN > ctx && key0 < it.n_pages * kPage) ||
+                           (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
             const int vst = vr.stage(blk);
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bs->v_full[vst], vr.use(blk) & 1))) {
               ok = false;
               break;
             }
-            if (key >= ctx && key < min(it.n_pages, it.page_end) * kPage) {
+            if ((key >= ctx && key < min(it.n_pages, it.page_end) * kPage) ||
+                (WIN && key >= z0 && key < z1)) {
               unsigned char *vrow = v_stage(vst) + (r / kPage) * C::PAGE_BYTES + (r % kPage) * 128;
 #pragma unroll
               for (int pl = 0; pl < C::PANELS; ++pl)
@@ -1670,7 +1751,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-template <int KVM, int D, int G>
+template <int KVM, int D, int G, bool WIN>
 cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream) {
   using C = StepCfg<D>;
   auto encode = encode_fn();
@@ -1748,7 +1829,7 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   }
   static bool configured = false;
   if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G>,
+    cudaError_t e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G, WIN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     configured = true;
@@ -1758,13 +1839,13 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   const int side_ctas = (int)std::min<int64_t>(w.grid, (side + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
   static bool plan_configured = false;
   if (!plan_configured) {
-    cudaError_t e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G>,
+    cudaError_t e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G, WIN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)plan_smem_bytes(kDecodeMaxSeqs));
     if (e != cudaSuccess) return e;
     plan_configured = true;
   }
-  attn_plan_kernel<KVM, G><<<1 + side_ctas, kPlanThreads, plan_smem_bytes(p.num_seqs), stream>>>(p, w);
+  attn_plan_kernel<KVM, G, WIN><<<1 + side_ctas, kPlanThreads, plan_smem_bytes(p.num_seqs), stream>>>(p, w);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // ... then the step, allowed to start while the plan finishes
@@ -1778,27 +1859,27 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_step_kernel<KVM, D, G>, p, w, tq, tqd, tk, tv, (int)rows);
+  return cudaLaunchKernelEx(&cfg, attn_step_kernel<KVM, D, G, WIN>, p, w, tq, tqd, tk, tv, (int)rows);
 }
 
 }  // namespace
 
-template <int KVM>
+template <int KVM, bool WIN>
 cudaError_t launch_step(const AttnParams &p, const StepWs &w, cudaStream_t stream) {
   const int G = p.Hq / p.Hkv;
   if (p.D == 128) {
     switch (G) {
-      case 1: return launch_dg<KVM, 128, 1>(p, w, stream);
-      case 2: return launch_dg<KVM, 128, 2>(p, w, stream);
-      case 4: return launch_dg<KVM, 128, 4>(p, w, stream);
-      case 8: return launch_dg<KVM, 128, 8>(p, w, stream);
+      case 1: return launch_dg<KVM, 128, 1, WIN>(p, w, stream);
+      case 2: return launch_dg<KVM, 128, 2, WIN>(p, w, stream);
+      case 4: return launch_dg<KVM, 128, 4, WIN>(p, w, stream);
+      case 8: return launch_dg<KVM, 128, 8, WIN>(p, w, stream);
     }
   } else {
     switch (G) {
-      case 1: return launch_dg<KVM, 64, 1>(p, w, stream);
-      case 2: return launch_dg<KVM, 64, 2>(p, w, stream);
-      case 4: return launch_dg<KVM, 64, 4>(p, w, stream);
-      case 8: return launch_dg<KVM, 64, 8>(p, w, stream);
+      case 1: return launch_dg<KVM, 64, 1, WIN>(p, w, stream);
+      case 2: return launch_dg<KVM, 64, 2, WIN>(p, w, stream);
+      case 4: return launch_dg<KVM, 64, 4, WIN>(p, w, stream);
+      case 8: return launch_dg<KVM, 64, 8, WIN>(p, w, stream);
     }
   }
   return cudaErrorInvalidValue;

@@ -162,7 +162,8 @@ namespace cpa {
 int attention(const void *q, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *query_start_loc,
               const int32_t *seq_lens, int32_t num_seqs, float scale, void *out,
-              void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes) {
+              void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes,
+              const Window &win) {
   int rc = check_shape(desc);
   if (rc != CPA_OK) return rc;
   if (num_seqs < 0) return CPA_ERR_ARG;
@@ -204,6 +205,11 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.scale_log2 = scale * p.k_scale * 1.4426950408889634f;
   if (!(p.scale_log2 > 0.f) || p.scale_log2 > 3.0e38f) return CPA_ERR_ARG;
   p.max_splits = w.max_splits;
+  // positions stay below 2^30, and so do the window and the sinks: their sums
+  // and differences stay in 32 bits
+  if (win.window && (int64_t)p.max_pages * p.page_size > (1 << 30)) return CPA_ERR_UNSUPPORTED;
+  p.window = std::min(win.window, 1 << 30);
+  p.sinks = std::min(win.sinks, 1 << 30);
   p.status = reinterpret_cast<uint32_t *>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   int grid = 0;
@@ -242,9 +248,9 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     }
     if (w.q16) p.q16 = ws + w.q16;
     cudaError_t e;
-    if (p.kv_e4m3) e = launch_step<2>(p, sw, st);
-    else if (p.act_f16) e = launch_step<1>(p, sw, st);
-    else e = launch_step<0>(p, sw, st);
+    if (p.kv_e4m3) e = win.window ? launch_step<2, true>(p, sw, st) : launch_step<2, false>(p, sw, st);
+    else if (p.act_f16) e = win.window ? launch_step<1, true>(p, sw, st) : launch_step<1, false>(p, sw, st);
+    else e = win.window ? launch_step<0, true>(p, sw, st) : launch_step<0, false>(p, sw, st);
     return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
   }
   // row kernel: the append (if any) first, on the same stream
@@ -263,7 +269,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.part_o = reinterpret_cast<float *>(ws + w.part_o);
   p.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
   p.rows_mode = 0;
-  if (desc->dtype == CPA_F32) {
+  if (desc->dtype == CPA_F32 && !win.window) {
     // the chunk rows on the tensor cores (tf32), the decode rows on the row kernel
     if (launch_chunk_tf32(p, st) != cudaSuccess) return CPA_ERR_CUDA;
     p.rows_mode = 2;
@@ -282,6 +288,45 @@ extern "C" int cpa_attention_forward(const void *q, const void *k_cache, const v
                    out, stream, desc, NewRows{}, 0);
 }
 
+extern "C" int cpa_window_attention_forward(const void *q, const void *k_cache,
+                                            const void *v_cache, const int32_t *block_table,
+                                            const int32_t *query_start_loc,
+                                            const int32_t *seq_lens, int32_t num_seqs,
+                                            float scale, int32_t window, int32_t sinks,
+                                            void *out, void *stream, const cpa_desc *desc) {
+  if (window < 1 || sinks < 0) return CPA_ERR_ARG;
+  return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
+                   out, stream, desc, NewRows{}, 0, Window{window, sinks});
+}
+
+// The append's arguments of the two fused calls; CPA_OK with no rows: nothing to do.
+static int append_args(const void *k, const void *v, const int64_t *slot_mapping,
+                       int32_t num_seqs, const cpa_desc *desc, NewRows *nr) {
+  int rc = check_shape(desc);
+  if (rc != CPA_OK) return rc;
+  if (num_seqs < 0) return CPA_ERR_ARG;
+  if (num_seqs == 0 || desc->num_tokens == 0) return CPA_OK;
+  if (!k || !v || !slot_mapping) return CPA_ERR_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8)) return CPA_ERR_ARG;
+  nr->k = k;
+  nr->v = v;
+  nr->slots = slot_mapping;
+  return CPA_OK;
+}
+
+extern "C" int cpa_append_window_attention_forward(
+    const void *q, const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,
+    void *v_cache, const int32_t *block_table, const int32_t *query_start_loc,
+    const int32_t *seq_lens, int32_t num_seqs, float scale, int32_t window, int32_t sinks,
+    void *out, void *stream, const cpa_desc *desc) {
+  if (window < 1 || sinks < 0) return CPA_ERR_ARG;
+  NewRows nr;
+  const int rc = append_args(k, v, slot_mapping, num_seqs, desc, &nr);
+  if (rc != CPA_OK || !nr.k) return rc;
+  return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
+                   out, stream, desc, nr, 0, Window{window, sinks});
+}
+
 extern "C" int cpa_append_attention_forward(const void *q, const void *k, const void *v,
                                             const int64_t *slot_mapping, void *k_cache,
                                             void *v_cache, const int32_t *block_table,
@@ -289,16 +334,9 @@ extern "C" int cpa_append_attention_forward(const void *q, const void *k, const 
                                             const int32_t *seq_lens, int32_t num_seqs,
                                             float scale, void *out, void *stream,
                                             const cpa_desc *desc) {
-  int rc = check_shape(desc);
-  if (rc != CPA_OK) return rc;
-  if (num_seqs < 0) return CPA_ERR_ARG;
-  if (num_seqs == 0 || desc->num_tokens == 0) return CPA_OK;
-  if (!k || !v || !slot_mapping) return CPA_ERR_ARG;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8)) return CPA_ERR_ARG;
   NewRows nr;
-  nr.k = k;
-  nr.v = v;
-  nr.slots = slot_mapping;
+  const int rc = append_args(k, v, slot_mapping, num_seqs, desc, &nr);
+  if (rc != CPA_OK || !nr.k) return rc;
   return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
                    out, stream, desc, nr, 0);
 }

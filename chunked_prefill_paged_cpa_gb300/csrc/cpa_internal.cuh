@@ -88,6 +88,9 @@ struct AttnParams {
   int max_pages;
   float scale_log2;          // scale * log2(e): scores live in the log2 domain
   int max_splits;
+  // Sliding window (0: none): the row at position x sees key j <= x when
+  // j < sinks or j > x - window.
+  int window, sinks;
   int rows_mode;              // row kernel: 0 all tokens, 1 only q_len > 1, 2 only q_len == 1
   // Fused append (cpa_append_attention_forward, step kernel): the step's new
   // k/v rows [num_tokens][Hkv][D] and their cache slots; the plan kernel
@@ -116,13 +119,19 @@ struct NewRows {
   const int64_t *slots = nullptr;
 };
 
+// Which keys a row sees (include/cpa.h); window 0: every key up to its own.
+struct Window {
+  int32_t window = 0, sinks = 0;
+};
+
 // The attention call behind every entry point (cpa_api.cu): validates the
 // arguments, optionally zeroes the first clear_bytes of the workspace on the
 // stream once they pass, then launches.
 int attention(const void *q, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *query_start_loc,
               const int32_t *seq_lens, int32_t num_seqs, float scale, void *out,
-              void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes);
+              void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes,
+              const Window &win = Window{});
 
 // Append of new rows; `quant` 0: copy elem_bytes-wide elements; 1 / 2: E4M3
 // codes of bf16 / binary16 rows divided by k_scale (K) and v_scale (V).
@@ -145,7 +154,8 @@ int sm_count(int device);
 // 16-bit queries, head_dim 64/128, GQA group 1/2/4/8.  KVM 0: bf16 queries and
 // caches; 1: binary16 queries and caches; 2: E4M3 caches.
 bool step_path(int dtype, int D, int G);
-template <int KVM>
+// WIN: with a sliding window (p.window >= 1).
+template <int KVM, bool WIN>
 cudaError_t launch_step(const AttnParams &p, const StepWs &w, cudaStream_t stream);
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -8,6 +8,7 @@ runs in the library's CUDA kernels; there is no other implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -79,6 +80,11 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.cpa_attention_forward.restype = ctypes.c_int
         lib.cpa_append_attention_forward.argtypes = [P, P, P, P, P, P, P, P, P, I32, F, P, P, D]
         lib.cpa_append_attention_forward.restype = ctypes.c_int
+        lib.cpa_window_attention_forward.argtypes = [P, P, P, P, P, P, I32, F, I32, I32, P, P, D]
+        lib.cpa_window_attention_forward.restype = ctypes.c_int
+        lib.cpa_append_window_attention_forward.argtypes = [P, P, P, P, P, P, P, P, P, I32, F, I32,
+                                                            I32, P, P, D]
+        lib.cpa_append_window_attention_forward.restype = ctypes.c_int
         lib.cpa_attention_forward_noalloc.argtypes = [P, P, P, P, P, P, I32, F, P, P, D]
         lib.cpa_attention_forward_noalloc.restype = ctypes.c_int
         lib.cpa_read_device_status.argtypes = [D, P, ctypes.POINTER(I32)]
@@ -120,6 +126,23 @@ def cpa_append_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, block_
                                                    block_table, query_start_loc, seq_lens,
                                                    int(num_seqs), float(scale), out, stream,
                                                    ctypes.byref(desc)))
+
+
+def cpa_window_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                                 num_seqs, scale, window, sinks, out, stream,
+                                 desc: CpaDesc) -> int:
+    return int(load().cpa_window_attention_forward(q, k_cache, v_cache, block_table,
+                                                   query_start_loc, seq_lens, int(num_seqs),
+                                                   float(scale), int(window), int(sinks), out,
+                                                   stream, ctypes.byref(desc)))
+
+
+def cpa_append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, block_table,
+                                        query_start_loc, seq_lens, num_seqs, scale, window, sinks,
+                                        out, stream, desc: CpaDesc) -> int:
+    return int(load().cpa_append_window_attention_forward(
+        q, k, v, slot_mapping, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+        int(num_seqs), float(scale), int(window), int(sinks), out, stream, ctypes.byref(desc)))
 
 
 def cpa_attention_forward_noalloc(q, k_cache, v_cache, block_table, query_start_loc,
@@ -250,6 +273,101 @@ def append_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, block_tabl
                                       scale, _ptr(out), _stream(stream), desc)
     if rc != CPA_OK:
         raise CpaError(rc, "cpa_append_attention_forward")
+    return out
+
+
+def _on(t: torch.Tensor, stream):
+    """Context that makes ``t``'s device the current one, and the stream to use
+    there: the one given, else torch's current stream of that device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    elif getattr(stream, "device", t.device) != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), _stream(stream)
+    return torch.cuda.device(t.device), _stream(stream)
+
+
+def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    """Raises unless ``t`` is a contiguous tensor of this dtype and shape (a
+    None entry matches any size) on ``device``: the library takes bare pointers."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected {device}, a CUDA device")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {shape} (None: any size)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _check_caches(k_cache, v_cache) -> None:
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected "
+                         "[num_pages, num_kv_heads, page_size, head_dim]")
+    _expect("k_cache", k_cache, k_cache.dtype, k_cache.shape, k_cache.device)
+    _expect("v_cache", v_cache, k_cache.dtype, k_cache.shape, k_cache.device)
+
+
+def _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, workspace, out,
+                 k_scale, v_scale):
+    """Checks of the windowed calls' tensors; (out, descriptor)."""
+    dev, dt = k_cache.device, q.dtype
+    if k_cache.dtype != torch.uint8 and k_cache.dtype != dt:
+        raise TypeError(f"q is {dt}, the caches are {k_cache.dtype}")
+    _check_caches(k_cache, v_cache)
+    _expect("q", q, dt, (None, None, k_cache.shape[3]), dev)
+    _expect("seq_lens", seq_lens, torch.int32, (None,), dev)
+    _expect("block_table", block_table, torch.int32, (seq_lens.shape[0], None), dev)
+    _expect("query_start_loc", query_start_loc, torch.int32, (seq_lens.shape[0] + 1,), dev)
+    _expect("workspace", workspace, torch.uint8, (None,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect("out", out, dt, q.shape, dev)
+    return out, make_desc(k_cache, q.shape[1], q.shape[0], block_table.shape[1], workspace, dt,
+                          k_scale, v_scale)
+
+
+def window_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, scale,
+                             workspace, window, sinks=0, out=None, stream=None, k_scale=1.0,
+                             v_scale=1.0) -> torch.Tensor:
+    """Attention of the packed batch where the row at position x sees position
+    j <= x when j < sinks or j > x - window.  Takes the workspace of
+    ``workspace_for``; block_table entries of pages no row sees are not read."""
+    out, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                             workspace, out, k_scale, v_scale)
+    ctx, st = _on(k_cache, stream)
+    with ctx:
+        rc = cpa_window_attention_forward(_ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(block_table), _ptr(query_start_loc),
+                                          _ptr(seq_lens), seq_lens.shape[0], scale, window, sinks,
+                                          _ptr(out), st, desc)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_window_attention_forward")
+    return out
+
+
+def append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, block_table,
+                                    query_start_loc, seq_lens, scale, workspace, window, sinks=0,
+                                    out=None, stream=None, k_scale=1.0,
+                                    v_scale=1.0) -> torch.Tensor:
+    """kv_append followed by window_attention_forward, as one C-ABI call."""
+    out, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                             workspace, out, k_scale, v_scale)
+    rows = (q.shape[0], k_cache.shape[1], k_cache.shape[3])
+    _expect("k", k, q.dtype, rows, k_cache.device)
+    _expect("v", v, q.dtype, rows, k_cache.device)
+    _expect("slot_mapping", slot_mapping, torch.int64, rows[:1], k_cache.device)
+    ctx, st = _on(k_cache, stream)
+    with ctx:
+        rc = cpa_append_window_attention_forward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
+            _ptr(block_table), _ptr(query_start_loc), _ptr(seq_lens), seq_lens.shape[0], scale,
+            window, sinks, _ptr(out), st, desc)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_append_window_attention_forward")
     return out
 
 

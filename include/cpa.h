@@ -190,6 +190,46 @@ int cpa_append_attention_forward(const void *q, const void *k, const void *v,
                                  const int32_t *seq_lens, int32_t num_seqs, float scale,
                                  void *out, void *stream, const cpa_desc *desc);
 
+/* ---- Attention with a sliding window and sinks ------------------------------
+ * The pages have no counterpart to these calls, nor to the page operators
+ * below: library extensions for serving with a bounded cache.
+ *
+ * The query row at position x of its sequence (x = seq_lens[s] - q_len + i for
+ * row i) sees cache position j when j <= x and (j < sinks or j > x - window):
+ * the last `window` positions, its own among them, and the first `sinks`
+ * positions, which stay visible for good.  Everything else is as in
+ * cpa_attention_forward: the whole packed batch of chunks and decodes, every
+ * dtype and cache storage, the workspace (cpa_workspace_bytes), the arguments'
+ * checks, and the status word.
+ *  - window >= 1 (so no row is without a visible key), sinks >= 0; CPA_ERR_ARG
+ *    otherwise.  A window of at least the context is plain causal attention.
+ *    max_pages_per_seq * page_size is at most 2^30 (CPA_ERR_UNSUPPORTED).
+ *  - The cost is that of the visible keys, whatever the length of the sequence.
+ *    Only pages that hold a position some row of the sequence sees are looked
+ *    up and read: block_table entries of the others may be anything (pages
+ *    given back with cpa_release_pages have -1 there).
+ *  - Keys and values no row of a 256-row group (256 / G consecutive tokens of a
+ *    chunk; a decode on its own) sees may hold anything, NaN included.  Inside
+ *    a chunk a non-finite V that one row of the group sees can make the outputs
+ *    of the group's other rows non-finite, as in cpa_attention_forward.
+ *  - fp32 activations are computed in fp32 throughout (no tf32 products). */
+int cpa_window_attention_forward(const void *q, const void *k_cache, const void *v_cache,
+                                 const int32_t *block_table, const int32_t *query_start_loc,
+                                 const int32_t *seq_lens, int32_t num_seqs, float scale,
+                                 int32_t window, int32_t sinks, void *out, void *stream,
+                                 const cpa_desc *desc);
+
+/* cpa_kv_append and cpa_window_attention_forward of one step in one call, as
+ * cpa_append_attention_forward is of cpa_attention_forward: the same results
+ * as the two calls, fused where the step kernel takes the shape. */
+int cpa_append_window_attention_forward(const void *q, const void *k, const void *v,
+                                        const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                                        const int32_t *block_table,
+                                        const int32_t *query_start_loc, const int32_t *seq_lens,
+                                        int32_t num_seqs, float scale, int32_t window,
+                                        int32_t sinks, void *out, void *stream,
+                                        const cpa_desc *desc);
+
 /* Size of the scratch array built into the library for
  * cpa_attention_forward_noalloc: 64 MiB of device memory on every GPU that
  * loads the library, held until the process exits. */

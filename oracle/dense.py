@@ -16,15 +16,20 @@ import numpy as np
 from scipy.special import softmax
 
 
-def visibility(q_len: int, ctx: int) -> np.ndarray:
-    """[q_len, ctx] matrix: True where query row i may attend to key j."""
+def visibility(q_len: int, ctx: int, window: int | None = None, sinks: int = 0) -> np.ndarray:
+    """[q_len, ctx] matrix: True where query row i may attend to key j.  With a
+    sliding window only the last ``window`` positions up to the row's own and
+    the first ``sinks`` positions."""
     pos_q = np.arange(ctx - q_len, ctx)[:, None]   # absolute position of row i
     pos_k = np.arange(ctx)[None, :]
-    return pos_k <= pos_q
+    seen = pos_k <= pos_q
+    if window is not None:
+        seen &= (pos_k > pos_q - window) | (pos_k < sinks)
+    return seen
 
 
 def attention_dense(q: np.ndarray, k_seqs: list, v_seqs: list, q_lens: list,
-                    scale: float) -> np.ndarray:
+                    scale: float, window: int | None = None, sinks: int = 0) -> np.ndarray:
     """q: [T, Hq, D] (packed, sequences in order); k_seqs[s], v_seqs[s]:
     [ctx_s, Hkv, D].  Returns [T, Hq, D] float64."""
     q = np.asarray(q, dtype=np.float64)
@@ -36,7 +41,7 @@ def attention_dense(q: np.ndarray, k_seqs: list, v_seqs: list, q_lens: list,
         V = np.asarray(v_seqs[s], dtype=np.float64)
         ctx, Hkv, _ = K.shape
         group = Hq // Hkv
-        mask = visibility(q_len, ctx)
+        mask = visibility(q_len, ctx, window, sinks)
         for h in range(Hq):
             g = h // group
             Qh = q[start:start + q_len, h, :]                  # [q_len, D]

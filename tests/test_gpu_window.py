@@ -1,0 +1,183 @@
+"""Attention with a sliding window and sinks on the GPU, against the formula in 64 bits."""
+import pytest
+import torch
+
+from chunked_prefill_paged_cpa_gb300 import ops
+from window_support import make_batch, reference, tolerance
+
+pytestmark = pytest.mark.gpu
+
+MODES = ["bf16", "f16", "f32", "bf16-e4m3", "f16-e4m3"]
+# (window, sinks): one key; sinks alone; page edges; odd; past a tile; past every context; all sinks
+WINDOWS = [(1, 0), (1, 1), (16, 0), (17, 4), (100, 33), (128, 16), (129, 130), (1000, 4), (5000, 0), (3, 5000)]
+# decodes of one key up to several pages, chunks from scratch, one-page chunks, chunks with an unaligned prefix
+MIXED = ([1, 1, 1, 37, 130, 1, 2, 300], [1, 17, 700, 37, 900, 2049, 50, 300])
+
+
+def workspace(b):
+    return ops.workspace_for(b["k_cache"], b["q"].shape[1], b["table"].shape[1], len(b["q_lens"]),
+                             b["q"].shape[0], act_dtype=b["q"].dtype)
+
+
+def window_call(b, ws, append=False, out=None):
+    rest = (b["k_cache"], b["v_cache"], b["table"], b["starts"], b["lens"], b["scale"], ws, b["window"], b["sinks"])
+    if append:
+        return ops.append_window_attention_forward(b["q"], b["k"], b["v"], b["slots"], *rest, out=out, **b["scales"])
+    return ops.window_attention_forward(b["q"], *rest, out=out, **b["scales"])
+
+
+def check(b, got, what=""):
+    want, size = reference(b)
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all(), f"{what}: non-finite output"
+    over = err > tolerance(b, want, size)
+    assert not over.any(), f"{what}: {int(over.sum())} outputs off, worst {float(err[over].max()):.3e}"
+
+
+def status(b, ws):
+    return ops.device_status(b["k_cache"], b["q"].shape[1], b["table"].shape[1], ws)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_mixed_batch(cuda_device, mode, window, sinks):
+    b = make_batch(*MIXED, 8, 2, 128, mode, window, sinks, 11 + window, cuda_device)
+    ws = workspace(b)
+    out = window_call(b, ws)
+    assert status(b, ws) == ops.CPA_OK
+    check(b, out, f"{mode} {window} {sinks}")
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 3), (4, 2), (12, 3), (8, 1), (32, 8)])
+def test_heads(cuda_device, mode, d, hq, hkv):
+    b = make_batch([1, 70, 1, 1], [333, 200, 16, 1500], hq, hkv, d, mode, 77, 5, 500 + hq, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{mode} {hq}/{hkv} {d}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("seed", range(4))
+def test_ragged(cuda_device, mode, seed):
+    """Random lengths, windows and sinks, several chunks in one step."""
+    g = torch.Generator().manual_seed(900 + seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    q_lens = [r(1, 400) if r(0, 2) == 0 else 1 for _ in range(9)]
+    seq_lens = [q + r(0, 2500) for q in q_lens]
+    b = make_batch(q_lens, seq_lens, 8, 2, 64, mode, r(1, 700), r(0, 60), 950 + seed, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{mode} {q_lens} {seq_lens}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_append_in_the_same_call(cuda_device, mode):
+    """The cache's bytes and the output's bits are those of the two separate calls."""
+    b = make_batch(*MIXED, 8, 2, 128, mode, 150, 4, 31, cuda_device)
+    whole = [b["k_cache"].clone(), b["v_cache"].clone()]
+    page, off = b["slots"] // 16, b["slots"] % 16
+    for c in ("k_cache", "v_cache"):
+        b[c][page, :, off] = 0x7F if b[c].dtype == torch.uint8 else float("nan")
+    k1, v1 = b["k_cache"].clone(), b["v_cache"].clone()
+    ops.kv_append(b["k"], b["v"], b["slots"], k1, v1, **b["scales"])
+    out1 = window_call(dict(b, k_cache=k1, v_cache=v1), workspace(b))
+    out2 = window_call(b, workspace(b), append=True)
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    for got, sep, want in ((b["k_cache"], k1, whole[0]), (b["v_cache"], v1, whole[1])):
+        assert torch.equal(raw(got), raw(sep)) and torch.equal(raw(got), raw(want))
+    assert torch.equal(raw(out1), raw(out2))
+    check(b, out2, mode)
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "bf16-e4m3"])
+def test_long_context_costs_only_its_window(cuda_device, mode):
+    """Decodes and a chunk far behind their sinks: only the visible pages exist."""
+    b = make_batch([1, 40, 1], [100_000, 70_000, 65_537], 4, 1, 64, mode, 200, 20, 7, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), mode)
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", ["bf16", "bf16-e4m3"])
+def test_split_over_the_context(cuda_device, mode):
+    """One long decode and one short chunk with a long window: both split over many CTAs and merged."""
+    b = make_batch([1, 20], [4090, 4000], 8, 1, 128, mode, 3900, 40, 8, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), mode)
+
+
+def test_many_sequences(cuda_device):
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(1, 60, (4096,), generator=g).tolist()
+    b = make_batch([1] * 4096, lens, 4, 2, 64, "bf16", 21, 3, 4, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws))
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "f16-e4m3"])
+def test_jumps_of_the_logits_at_the_windows_edge(cuda_device, mode):
+    """Large keys just outside the window (they must not move the softmax) and just inside."""
+    b = make_batch([1, 90], [500, 400], 4, 2, 64, mode, 100, 7, 21, cuda_device, poison=False)
+    q0 = b["q"][0, 0].double() * 4
+    for s, n in enumerate(b["seq_lens"]):
+        for pos in (7, n - b["q_lens"][s] - 100, n - 100, n - 101):
+            page, off = int(b["table"][s, pos // 16]), pos % 16
+            row = q0.to(b["q"].dtype).double()
+            if b["k_cache"].dtype == torch.uint8:
+                codes = (row / 2.0 ** -6).clamp(-448, 448).to(torch.float8_e4m3fn)
+                b["k_cache"][page, :, off] = codes.view(torch.uint8)
+                b["dense"][s][0][pos] = codes.double() * 2.0 ** -6
+            else:
+                b["k_cache"][page, :, off] = row.to(b["k_cache"].dtype)
+                b["dense"][s][0][pos] = row.to(b["k_cache"].dtype).double()
+    want, size = reference(b)
+    got = window_call(b, workspace(b)).double()
+    # these scores reach |s| = 4 sum |q|^2 scale < 64: the fp32 bound of the scores grows by 64 / 11 < 8
+    tol = tolerance(b, want, size) + 7 * 2.0 ** -13 * size
+    assert ((got - want).abs() <= tol).all()
+
+
+def test_bad_page_inside_the_window_is_reported(cuda_device):
+    b = make_batch([1], [300], 4, 2, 64, "bf16", 50, 4, 5, cuda_device)
+    ws = workspace(b)
+    b["table"][0, 300 // 16] = 1 << 20
+    window_call(b, ws)
+    assert status(b, ws) == ops.CPA_ERR_DEVICE
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32"])
+def test_captured_and_replayed(cuda_device, mode):
+    b = make_batch(*MIXED, 8, 2, 64, mode, 60, 4, 41, cuda_device)
+    ws, out = workspace(b), torch.empty_like(b["q"])
+    eager = window_call(b, ws, append=True).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        window_call(b, ws, append=True, out=out)
+    for _ in range(3):
+        out.zero_()
+        ws[256:].random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+    b["q"].mul_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(b, out, "replayed on new queries")
+
+
+def test_on_another_stream(cuda_device):
+    b = make_batch(*MIXED, 8, 2, 64, "bf16", 60, 4, 43, cuda_device)
+    want = window_call(b, workspace(b))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ws = workspace(b)
+    s.wait_stream(torch.cuda.current_stream())
+    got = ops.window_attention_forward(b["q"], b["k_cache"], b["v_cache"], b["table"], b["starts"], b["lens"],
+                                       b["scale"], ws, 60, 4, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
