@@ -81,7 +81,7 @@ WorkspaceLayout workspace_layout(const cpa_desc &d, int num_seqs) {
 }
 
 // Shape checks shared by both calls.
-static int check_shape(const cpa_desc *d) {
+int check_shape(const cpa_desc *d) {
   if (!d) return CPA_ERR_ARG;
   if (d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->head_dim <= 0 ||
       d->page_size <= 0 || d->num_pages <= 0 || d->num_tokens < 0)

@@ -15,6 +15,8 @@ enum : uint32_t {
   STATUS_BAD_PAGE = 1u,   // block_table entry outside [0, num_pages)
   STATUS_BAD_SLOT = 2u,   // slot_mapping entry >= num_pages * page_size
   STATUS_TIMEOUT = 4u,    // a bounded wait gave up
+  STATUS_BAD_ROW = 8u,    // page operators: a row that cannot be forked, extended or released
+  STATUS_NO_PAGES = 16u,  // cpa_extend_sequences: fewer free pages than the step needs
 };
 
 // Workspace layout (byte offsets from desc->workspace, all 256-aligned).
@@ -146,6 +148,9 @@ cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t s
 // fp32 steps: the chunk rows (q_len > 1) on the tensor cores, kind::tf32
 // (attn_chunk_tf32.cu); the decode rows then go to the row kernel (rows_mode 2).
 cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
+
+// Checks of the cache's shape shared by the calls (cpa_api.cu).
+int check_shape(const cpa_desc *d);
 
 // Number of SMs of a device (cached); 0 if it cannot be queried.
 int sm_count(int device);

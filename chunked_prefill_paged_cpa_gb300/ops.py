@@ -85,6 +85,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.cpa_append_window_attention_forward.argtypes = [P, P, P, P, P, P, P, P, P, I32, F, I32,
                                                             I32, P, P, D]
         lib.cpa_append_window_attention_forward.restype = ctypes.c_int
+        lib.cpa_pages_workspace_bytes.argtypes = [ctypes.c_int64]
+        lib.cpa_pages_workspace_bytes.restype = Z
+        lib.cpa_copy_pages.argtypes = [P, P, P, I32, P, P, D, P]
+        lib.cpa_copy_pages.restype = ctypes.c_int
+        lib.cpa_fork_sequences.argtypes = [P, P, I32, P, P, I32, P, D, P]
+        lib.cpa_fork_sequences.restype = ctypes.c_int
+        lib.cpa_extend_sequences.argtypes = [P, P, I32, P, P, P, P, P, P, D, P]
+        lib.cpa_extend_sequences.restype = ctypes.c_int
+        lib.cpa_release_pages.argtypes = [P, I32, P, P, I32, I32, I32, P, D, P]
+        lib.cpa_release_pages.restype = ctypes.c_int
+        lib.cpa_compact_pages.argtypes = [P, I32, P, P, P, P, D, P]
+        lib.cpa_compact_pages.restype = ctypes.c_int
         lib.cpa_attention_forward_noalloc.argtypes = [P, P, P, P, P, P, I32, F, P, P, D]
         lib.cpa_attention_forward_noalloc.restype = ctypes.c_int
         lib.cpa_read_device_status.argtypes = [D, P, ctypes.POINTER(I32)]
@@ -143,6 +155,41 @@ def cpa_append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache,
     return int(load().cpa_append_window_attention_forward(
         q, k, v, slot_mapping, k_cache, v_cache, block_table, query_start_loc, seq_lens,
         int(num_seqs), float(scale), int(window), int(sinks), out, stream, ctypes.byref(desc)))
+
+
+def cpa_pages_workspace_bytes(num_pages: int) -> int:
+    return int(load().cpa_pages_workspace_bytes(int(num_pages)))
+
+
+def cpa_copy_pages(src, dst, num_pairs, max_pairs, k_cache, v_cache, desc: CpaDesc, stream) -> int:
+    return int(load().cpa_copy_pages(src, dst, num_pairs, int(max_pairs), k_cache, v_cache,
+                                     ctypes.byref(desc), stream))
+
+
+def cpa_fork_sequences(parents, children, num_forks, block_table, seq_lens, num_rows, page_refs,
+                       desc: CpaDesc, stream) -> int:
+    return int(load().cpa_fork_sequences(parents, children, int(num_forks), block_table, seq_lens,
+                                         int(num_rows), page_refs, ctypes.byref(desc), stream))
+
+
+def cpa_extend_sequences(query_start_loc, seq_lens, num_seqs, block_table, page_refs,
+                         slot_mapping, copy_src, copy_dst, counts, desc: CpaDesc, stream) -> int:
+    return int(load().cpa_extend_sequences(query_start_loc, seq_lens, int(num_seqs), block_table,
+                                           page_refs, slot_mapping, copy_src, copy_dst, counts,
+                                           ctypes.byref(desc), stream))
+
+
+def cpa_release_pages(rows, num_released, block_table, seq_lens, num_rows, window, sinks,
+                      page_refs, desc: CpaDesc, stream) -> int:
+    return int(load().cpa_release_pages(rows, int(num_released), block_table, seq_lens,
+                                        int(num_rows), int(window), int(sinks), page_refs,
+                                        ctypes.byref(desc), stream))
+
+
+def cpa_compact_pages(block_table, num_rows, page_refs, copy_src, copy_dst, counts,
+                      desc: CpaDesc, stream) -> int:
+    return int(load().cpa_compact_pages(block_table, int(num_rows), page_refs, copy_src, copy_dst,
+                                        counts, ctypes.byref(desc), stream))
 
 
 def cpa_attention_forward_noalloc(q, k_cache, v_cache, block_table, query_start_loc,
@@ -369,6 +416,124 @@ def append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, blo
     if rc != CPA_OK:
         raise CpaError(rc, "cpa_append_window_attention_forward")
     return out
+
+
+def pages_workspace_for(num_pages: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for the table operators of a pool of ``num_pages``."""
+    n = cpa_pages_workspace_bytes(num_pages)
+    if n == 0:
+        raise CpaError(CPA_ERR_ARG, "cpa_pages_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _pool_desc(block_table, page_refs, workspace, num_tokens: int = 0) -> CpaDesc:
+    """Checks of the tensors every table operator takes; its descriptor."""
+    dev = page_refs.device
+    _expect("page_refs", page_refs, torch.int32, (None,), dev)
+    _expect("block_table", block_table, torch.int32, (None, None), dev)
+    _expect("workspace", workspace, torch.uint8, (None,), dev)
+    return CpaDesc(1, 1, 64, 16, page_refs.shape[0], block_table.shape[1], CPA_BF16, num_tokens,
+                   workspace.data_ptr(), workspace.shape[0], CPA_KV_SAME, 0.0, 0.0)
+
+
+def _check_pairs(src, dst, least: int, device) -> None:
+    _expect("copy_src", src, torch.int32, (None,), device)
+    _expect("copy_dst", dst, torch.int32, (None,), device)
+    if src.shape[0] < least or dst.shape[0] < least:
+        raise ValueError(f"copy_src and copy_dst need {least} entries, they have {src.shape[0]} "
+                         f"and {dst.shape[0]}")
+
+
+def copy_pages(src, dst, k_cache, v_cache, num_pairs=None, workspace=None, stream=None) -> None:
+    """Copies pages ``src[i]`` of both caches to pages ``dst[i]``, for every i,
+    or for i below ``num_pairs[0]`` (an int32 tensor on the device)."""
+    dev = k_cache.device
+    _check_caches(k_cache, v_cache)
+    _expect("src", src, torch.int32, (None,), dev)
+    _expect("dst", dst, torch.int32, src.shape, dev)
+    if num_pairs is not None:
+        _expect("num_pairs", num_pairs, torch.int32, (None,), dev)
+        if num_pairs.shape[0] < 1:
+            raise ValueError("num_pairs is empty")
+    if workspace is not None:
+        _expect("workspace", workspace, torch.uint8, (None,), dev)
+    desc = make_desc(k_cache, k_cache.shape[1], 0, 1, workspace)
+    ctx, st = _on(k_cache, stream)
+    with ctx:
+        rc = cpa_copy_pages(_ptr(src), _ptr(dst), _ptr(num_pairs), src.shape[0], _ptr(k_cache),
+                            _ptr(v_cache), desc, st)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_copy_pages")
+
+
+def fork_sequences(parents, children, block_table, seq_lens, page_refs, workspace,
+                   stream=None) -> None:
+    """Row ``children[i]`` becomes a copy of row ``parents[i]`` that shares its pages."""
+    desc = _pool_desc(block_table, page_refs, workspace)
+    dev = page_refs.device
+    _expect("parents", parents, torch.int32, (None,), dev)
+    _expect("children", children, torch.int32, parents.shape, dev)
+    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
+    ctx, st = _on(page_refs, stream)
+    with ctx:
+        rc = cpa_fork_sequences(_ptr(parents), _ptr(children), parents.shape[0], _ptr(block_table),
+                                _ptr(seq_lens), block_table.shape[0], _ptr(page_refs), desc, st)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_fork_sequences")
+
+
+def extend_sequences(query_start_loc, seq_lens, block_table, page_refs, slot_mapping, copy_src,
+                     copy_dst, counts, workspace, stream=None) -> None:
+    """Pages, slots and copies for a step's new tokens (``seq_lens`` counts
+    them): fills ``slot_mapping``, the pairs' list and ``counts`` = (pairs, pages
+    taken), the latter negative where the pool has too few."""
+    desc = _pool_desc(block_table, page_refs, workspace, slot_mapping.shape[0])
+    dev, n = page_refs.device, seq_lens.shape[0]
+    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
+    _expect("query_start_loc", query_start_loc, torch.int32, (n + 1,), dev)
+    _expect("slot_mapping", slot_mapping, torch.int64, (None,), dev)
+    _expect("counts", counts, torch.int32, (2,), dev)
+    _check_pairs(copy_src, copy_dst, n, dev)
+    ctx, st = _on(page_refs, stream)
+    with ctx:
+        rc = cpa_extend_sequences(_ptr(query_start_loc), _ptr(seq_lens), n, _ptr(block_table),
+                                  _ptr(page_refs), _ptr(slot_mapping), _ptr(copy_src),
+                                  _ptr(copy_dst), _ptr(counts), desc, st)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_extend_sequences")
+
+
+def release_pages(rows, block_table, seq_lens, page_refs, workspace, window=0, sinks=0,
+                  stream=None) -> None:
+    """Gives back the pages of ``rows`` (None: all rows): every page, or, with a
+    window, those that the queries to come do not see."""
+    desc = _pool_desc(block_table, page_refs, workspace)
+    dev = page_refs.device
+    if rows is not None:
+        _expect("rows", rows, torch.int32, (None,), dev)
+    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
+    n = block_table.shape[0] if rows is None else rows.shape[0]
+    ctx, st = _on(page_refs, stream)
+    with ctx:
+        rc = cpa_release_pages(_ptr(rows), n, _ptr(block_table), _ptr(seq_lens),
+                               block_table.shape[0], window, sinks, _ptr(page_refs), desc, st)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_release_pages")
+
+
+def compact_pages(block_table, page_refs, copy_src, copy_dst, counts, workspace,
+                  stream=None) -> None:
+    """Packs the pool's live pages to its front: ``counts`` = (pairs to copy, live pages)."""
+    desc = _pool_desc(block_table, page_refs, workspace)
+    dev = page_refs.device
+    _expect("counts", counts, torch.int32, (2,), dev)
+    _check_pairs(copy_src, copy_dst, page_refs.shape[0] // 2, dev)
+    ctx, st = _on(page_refs, stream)
+    with ctx:
+        rc = cpa_compact_pages(_ptr(block_table), block_table.shape[0], _ptr(page_refs),
+                               _ptr(copy_src), _ptr(copy_dst), _ptr(counts), desc, st)
+    if rc != CPA_OK:
+        raise CpaError(rc, "cpa_compact_pages")
 
 
 def device_status(k_cache, num_q_heads, max_pages_per_seq, workspace, stream=None) -> int:

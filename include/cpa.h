@@ -69,7 +69,10 @@ typedef enum {
  * counters itself.  Bits 1 and 2 mean the metadata is wrong; fix it before
  * re-running.  Bit 4 alone means the GPU did not run the kernel's CTAs to
  * completion in time (for instance a stream starved for longer than the wait
- * limit by other work); the same call can simply be issued again. */
+ * limit by other work); the same call can simply be issued again.
+ * The page operators also raise bit 8: a row that could not be forked,
+ * extended or released (left as it was), and bit 16: cpa_extend_sequences
+ * found too few free pages (nothing was changed). */
 
 typedef enum { CPA_F32 = 0, CPA_BF16 = 1, CPA_F16 = 2 } cpa_dtype;
 
@@ -229,6 +232,109 @@ int cpa_append_window_attention_forward(const void *q, const void *k, const void
                                         int32_t num_seqs, float scale, int32_t window,
                                         int32_t sinks, void *out, void *stream,
                                         const cpa_desc *desc);
+
+/* ---- Page operators --------------------------------------------------------
+ * Sequences that share pages, and a pool whose pages are given back, on the
+ * device: no call waits for the host, and all can be captured into a graph.
+ *
+ * State (device memory, the caller's):
+ *   block_table  int32 [num_rows][max_pages_per_seq]; entry c of a row holds
+ *                positions 16 c .. 16 c + 15, -1 (any negative value) where
+ *                the row holds no page
+ *   seq_lens     int32 [num_rows]
+ *   page_refs    int32 [num_pages], 16-byte aligned: how many block_table
+ *                entries hold the page; 0 = free
+ * block_table and seq_lens are those of the attention calls.  The results
+ * depend on the state alone: where pages are chosen, the lowest are taken, and
+ * rows count in their order.  One table and one page_refs may serve the caches
+ * of many layers: the table operators move no K or V, they list the copies to
+ * make, and cpa_copy_pages makes them, once per layer.
+ * The table operators read desc->num_pages, page_size (16), max_pages_per_seq
+ * (at most 2^26) and workspace: at least cpa_pages_workspace_bytes, 256-byte
+ * aligned, its first four bytes (the status word, cpa_read_device_status) zero
+ * before the first use.  Calls that may overlap on the GPU need workspaces of
+ * their own.  num_pages is below 2^27. */
+
+/* Workspace of the table operators for a pool of num_pages; 0 if out of range. */
+size_t cpa_pages_workspace_bytes(int64_t num_pages);
+
+/* For every pair i < n: page src[i] of k_cache and of v_cache is copied, bit
+ * for bit, to page dst[i].  n is max_pairs, or, with num_pairs not NULL, the
+ * device value *num_pairs (at most max_pairs count).  The pages in dst are
+ * distinct, and none of them is in src (the lists of cpa_extend_sequences and
+ * cpa_compact_pages are so); where they are not, those pages' contents are
+ * unspecified.  A pair that names a page outside [0, num_pages) is skipped and
+ * raises the status word when a workspace is given in desc.  Reads the cache's
+ * shape and type from desc, as cpa_kv_append does; max_pairs may be 0. */
+int cpa_copy_pages(const int32_t *src, const int32_t *dst, const int32_t *num_pairs,
+                   int32_t max_pairs, void *k_cache, void *v_cache, const cpa_desc *desc,
+                   void *stream);
+
+/* For every fork i: row children[i] becomes a copy of row parents[i], the
+ * length with it, and every page it holds gains a reference.  No page is
+ * copied, the partly filled last one neither: cpa_extend_sequences does that
+ * when one of its holders writes to it.  A parent may be forked many times.
+ * A child's row holds no page before the call, is no other child of the call
+ * and no parent in it; a fork whose child is not so, or with a row outside
+ * [0, num_rows), is left out whole and raises the status word.  At most 4096
+ * forks per call (CPA_ERR_UNSUPPORTED), and no more than num_rows. */
+int cpa_fork_sequences(const int32_t *parents, const int32_t *children, int32_t num_forks,
+                       int32_t *block_table, int32_t *seq_lens, int32_t num_rows,
+                       int32_t *page_refs, const cpa_desc *desc, void *stream);
+
+/* Makes room for a step's new tokens, which are described as for the attention
+ * calls: row s takes q_len = query_start_loc[s + 1] - query_start_loc[s] tokens
+ * (0: none), and seq_lens[s] counts them already.  In the order of the rows,
+ * and of the pages in each:
+ *  - where a position of the new tokens has no page, the row takes the lowest
+ *    page that was free before the call;
+ *  - where the first new token goes to a page that holds earlier tokens and has
+ *    other references left, the row gives its reference up, takes the lowest
+ *    free page instead, and the pair (old, new) is listed in copy_src,
+ *    copy_dst: the last of several rows that all write to a page keeps it;
+ *  - slot_mapping[t] is the slot of every new token t, as cpa_kv_append and
+ *    the fused attention calls take it.
+ * counts (int32 [2], device): the number of pairs listed, and of pages taken.
+ * The pairs have to be copied (cpa_copy_pages with num_pairs = counts, in every
+ * layer's cache) before the step's rows are appended.
+ * If fewer pages are free than the step needs, nothing is changed: every
+ * slot_mapping entry is -1, counts = {0, -needed}, and the status word is
+ * raised.  A row with q_len < 0, seq_lens[s] < q_len, more tokens than its
+ * block_table row or than desc->num_tokens can hold takes nothing, its tokens'
+ * slots are -1, and the status word is raised; so is it by an entry past the
+ * pool.  Tokens past the last row's have slot -1.
+ * num_seqs rows of block_table, at most 4096 (CPA_ERR_UNSUPPORTED);
+ * slot_mapping int64 [desc->num_tokens]; copy_src, copy_dst int32 [num_seqs],
+ * written up to the count. */
+int cpa_extend_sequences(const int32_t *query_start_loc, const int32_t *seq_lens,
+                         int32_t num_seqs, int32_t *block_table, int32_t *page_refs,
+                         int64_t *slot_mapping, int32_t *copy_src, int32_t *copy_dst,
+                         int32_t *counts, const cpa_desc *desc, void *stream);
+
+/* Gives pages of num_released rows back (rows: their numbers; NULL: rows 0 ..
+ * num_released - 1): the entries become -1 and their pages lose a reference.
+ *  - window >= 1: the pages that no query from position seq_lens[row] on sees
+ *    with this window and sinks (see cpa_window_attention_forward): those
+ *    wholly at or behind `sinks` and wholly before seq_lens[row] - window + 1.
+ *  - window = 0 (sinks = 0): every page; seq_lens[row] becomes 0.
+ * A row may be named twice.  A row outside [0, num_rows) is left out and
+ * raises the status word, as does an entry whose page is past the pool or
+ * counts as free. */
+int cpa_release_pages(const int32_t *rows, int32_t num_released, int32_t *block_table,
+                      int32_t *seq_lens, int32_t num_rows, int32_t window, int32_t sinks,
+                      int32_t *page_refs, const cpa_desc *desc, void *stream);
+
+/* Packs the pool: afterwards its m live pages are pages 0 .. m - 1.  The j-th
+ * free page below m takes the place of the j-th live page from m on; page_refs
+ * and every entry of block_table follow, and the pairs (old, new) are listed in
+ * copy_src, copy_dst (int32 [num_pages / 2] each, written up to the count), to
+ * be copied in every layer's cache before anything reads or writes it.
+ * counts (int32 [2], device): the number of pairs, and m.  An entry whose page
+ * counts as free or is past the pool stays as it is and raises the status
+ * word.  Any number of rows. */
+int cpa_compact_pages(int32_t *block_table, int32_t num_rows, int32_t *page_refs,
+                      int32_t *copy_src, int32_t *copy_dst, int32_t *counts,
+                      const cpa_desc *desc, void *stream);
 
 /* Size of the scratch array built into the library for
  * cpa_attention_forward_noalloc: 64 MiB of device memory on every GPU that
