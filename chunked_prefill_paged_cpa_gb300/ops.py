@@ -8,7 +8,6 @@ runs in the library's CUDA kernels; there is no other implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -57,6 +56,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libcpa.so.  Raises if it is not built (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -323,58 +324,94 @@ def append_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, block_tabl
     return out
 
 
-def _on(t: torch.Tensor, stream):
-    """Context that makes ``t``'s device the current one, and the stream to use
-    there: the one given, else torch's current stream of that device."""
+def _launch(where: str, fn, index: int, stream, args: tuple, desc: CpaDesc, desc_last: bool) -> None:
+    """Calls C entry point ``fn`` on device ``index`` (made current for the
+    call), on the stream given, else on torch's current stream of that device.
+    ``args``: what comes before the stream and the descriptor."""
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    elif getattr(stream, "device", t.device) != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), _stream(stream)
-    return torch.cuda.device(t.device), _stream(stream)
+        st = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        on = getattr(stream, "device", None)
+        if on is not None and on.index != index:
+            raise ValueError(f"the stream is on {on}, the tensors are on cuda:{index}")
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    tail = (st, ctypes.byref(desc)) if desc_last else (ctypes.byref(desc), st)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, *tail)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, *tail)
+    if rc != CPA_OK:
+        raise CpaError(rc, where)
 
 
-def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
-    """Raises unless ``t`` is a contiguous tensor of this dtype and shape (a
-    None entry matches any size) on ``device``: the library takes bare pointers."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device}, a CUDA device")
-    have = t.shape
-    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
-        raise ValueError(f"{name} has shape {tuple(have)}, expected {shape} (None: any size)")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+def _expect(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> int:
+    """The address of ``t``, a contiguous tensor of this dtype and shape on
+    CUDA device ``index``; raises if it is something else: the library takes
+    bare pointers.  (One condition on the way that every call takes: a step's
+    ten tensors cost 5 us in all.)"""
+    if (t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}, expected "
+                         f"{'a CUDA device' if index < 0 else f'cuda:{index}'}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} is not contiguous")
 
 
-def _check_caches(k_cache, v_cache) -> None:
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected "
-                         "[num_pages, num_kv_heads, page_size, head_dim]")
-    _expect("k_cache", k_cache, k_cache.dtype, k_cache.shape, k_cache.device)
-    _expect("v_cache", v_cache, k_cache.dtype, k_cache.shape, k_cache.device)
+def _sizes(name: str, t: torch.Tensor, dims: int) -> torch.Size:
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {dims} dimensions")
+    return shape
+
+
+_DTYPES = {torch.float32: CPA_F32, torch.bfloat16: CPA_BF16, torch.float16: CPA_F16}
+
+
+def _cache_desc(k_cache, num_q_heads, num_tokens, max_pages, workspace, dtype, k_scale, v_scale,
+                index):
+    """Checked addresses of a workspace (or None) in a cache's descriptor."""
+    num_pages, hkv, page, d = k_cache.shape
+    ws = nb = 0
+    if workspace is not None:
+        nb = _sizes("workspace", workspace, 1)[0]
+        ws = _expect("workspace", workspace, torch.uint8, (nb,), index)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if k_cache.dtype is torch.uint8:
+        return CpaDesc(num_q_heads, hkv, d, page, num_pages, max_pages, code, num_tokens, ws or None,
+                       nb, CPA_KV_E4M3, k_scale, v_scale)
+    return CpaDesc(num_q_heads, hkv, d, page, num_pages, max_pages, code, num_tokens, ws or None, nb,
+                   CPA_KV_SAME, 0.0, 0.0)
 
 
 def _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, workspace, out,
                  k_scale, v_scale):
-    """Checks of the windowed calls' tensors; (out, descriptor)."""
-    dev, dt = k_cache.device, q.dtype
-    if k_cache.dtype != torch.uint8 and k_cache.dtype != dt:
-        raise TypeError(f"q is {dt}, the caches are {k_cache.dtype}")
-    _check_caches(k_cache, v_cache)
-    _expect("q", q, dt, (None, None, k_cache.shape[3]), dev)
-    _expect("seq_lens", seq_lens, torch.int32, (None,), dev)
-    _expect("block_table", block_table, torch.int32, (seq_lens.shape[0], None), dev)
-    _expect("query_start_loc", query_start_loc, torch.int32, (seq_lens.shape[0] + 1,), dev)
-    _expect("workspace", workspace, torch.uint8, (None,), dev)
+    """Checks of the windowed calls' tensors: (out, device, addresses, descriptor)."""
+    dt, index = q.dtype, k_cache.get_device()
+    kdt = k_cache.dtype
+    if kdt is not torch.uint8 and kdt is not dt:
+        raise TypeError(f"q is {dt}, the caches are {kdt}")
+    cache = _sizes("k_cache", k_cache, 4)
+    tokens, heads, _ = _sizes("q", q, 3)
+    seqs, cols = _sizes("block_table", block_table, 2)
+    qs = (tokens, heads, cache[3])
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _expect("out", out, dt, q.shape, dev)
-    return out, make_desc(k_cache, q.shape[1], q.shape[0], block_table.shape[1], workspace, dt,
-                          k_scale, v_scale)
+    i32 = torch.int32
+    at = (_expect("q", q, dt, qs, index), _expect("k_cache", k_cache, kdt, cache, index),
+          _expect("v_cache", v_cache, kdt, cache, index),
+          _expect("block_table", block_table, i32, (seqs, cols), index),
+          _expect("query_start_loc", query_start_loc, i32, (seqs + 1,), index),
+          _expect("seq_lens", seq_lens, i32, (seqs,), index), seqs)
+    desc = _cache_desc(k_cache, heads, tokens, cols, workspace, dt, k_scale, v_scale, index)
+    return out, index, at, _expect("out", out, dt, qs, index), desc
 
 
 def window_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, scale,
@@ -383,16 +420,10 @@ def window_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, 
     """Attention of the packed batch where the row at position x sees position
     j <= x when j < sinks or j > x - window.  Takes the workspace of
     ``workspace_for``; block_table entries of pages no row sees are not read."""
-    out, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
-                             workspace, out, k_scale, v_scale)
-    ctx, st = _on(k_cache, stream)
-    with ctx:
-        rc = cpa_window_attention_forward(_ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                          _ptr(block_table), _ptr(query_start_loc),
-                                          _ptr(seq_lens), seq_lens.shape[0], scale, window, sinks,
-                                          _ptr(out), st, desc)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_window_attention_forward")
+    out, index, at, to, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc,
+                                            seq_lens, workspace, out, k_scale, v_scale)
+    _launch("cpa_window_attention_forward", load().cpa_window_attention_forward, index, stream,
+            (*at, scale, window, sinks, to), desc, True)
     return out
 
 
@@ -401,20 +432,13 @@ def append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, blo
                                     out=None, stream=None, k_scale=1.0,
                                     v_scale=1.0) -> torch.Tensor:
     """kv_append followed by window_attention_forward, as one C-ABI call."""
-    out, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
-                             workspace, out, k_scale, v_scale)
+    out, index, at, to, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc,
+                                            seq_lens, workspace, out, k_scale, v_scale)
     rows = (q.shape[0], k_cache.shape[1], k_cache.shape[3])
-    _expect("k", k, q.dtype, rows, k_cache.device)
-    _expect("v", v, q.dtype, rows, k_cache.device)
-    _expect("slot_mapping", slot_mapping, torch.int64, rows[:1], k_cache.device)
-    ctx, st = _on(k_cache, stream)
-    with ctx:
-        rc = cpa_append_window_attention_forward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
-            _ptr(block_table), _ptr(query_start_loc), _ptr(seq_lens), seq_lens.shape[0], scale,
-            window, sinks, _ptr(out), st, desc)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_append_window_attention_forward")
+    new = (_expect("k", k, q.dtype, rows, index), _expect("v", v, q.dtype, rows, index),
+           _expect("slot_mapping", slot_mapping, torch.int64, rows[:1], index))
+    _launch("cpa_append_window_attention_forward", load().cpa_append_window_attention_forward, index,
+            stream, (at[0], *new, *at[1:], scale, window, sinks, to), desc, True)
     return out
 
 
@@ -426,60 +450,55 @@ def pages_workspace_for(num_pages: int, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _pool_desc(block_table, page_refs, workspace, num_tokens: int = 0) -> CpaDesc:
-    """Checks of the tensors every table operator takes; its descriptor."""
-    dev = page_refs.device
-    _expect("page_refs", page_refs, torch.int32, (None,), dev)
-    _expect("block_table", block_table, torch.int32, (None, None), dev)
-    _expect("workspace", workspace, torch.uint8, (None,), dev)
-    return CpaDesc(1, 1, 64, 16, page_refs.shape[0], block_table.shape[1], CPA_BF16, num_tokens,
-                   workspace.data_ptr(), workspace.shape[0], CPA_KV_SAME, 0.0, 0.0)
+def _pool(block_table, page_refs, workspace, num_tokens: int = 0):
+    """Checks of the tensors every table operator takes: (device, rows,
+    addresses of the table and the references, descriptor)."""
+    index = page_refs.get_device()
+    (pages,), (rows, cols) = _sizes("page_refs", page_refs, 1), _sizes("block_table", block_table, 2)
+    nb = _sizes("workspace", workspace, 1)[0]
+    refs = _expect("page_refs", page_refs, torch.int32, (pages,), index)
+    table = _expect("block_table", block_table, torch.int32, (rows, cols), index)
+    ws = _expect("workspace", workspace, torch.uint8, (nb,), index)
+    return index, rows, table, refs, CpaDesc(1, 1, 64, 16, pages, cols, CPA_BF16, num_tokens, ws, nb,
+                                             CPA_KV_SAME, 0.0, 0.0)
 
 
-def _check_pairs(src, dst, least: int, device) -> None:
-    _expect("copy_src", src, torch.int32, (None,), device)
-    _expect("copy_dst", dst, torch.int32, (None,), device)
-    if src.shape[0] < least or dst.shape[0] < least:
-        raise ValueError(f"copy_src and copy_dst need {least} entries, they have {src.shape[0]} "
-                         f"and {dst.shape[0]}")
+def _pairs(src, dst, least: int, index: int) -> tuple:
+    ns, nd = _sizes("copy_src", src, 1)[0], _sizes("copy_dst", dst, 1)[0]
+    if min(ns, nd) < least:
+        raise ValueError(f"copy_src and copy_dst need {least} entries, they have {ns} and {nd}")
+    return (_expect("copy_src", src, torch.int32, (ns,), index),
+            _expect("copy_dst", dst, torch.int32, (nd,), index))
 
 
 def copy_pages(src, dst, k_cache, v_cache, num_pairs=None, workspace=None, stream=None) -> None:
     """Copies pages ``src[i]`` of both caches to pages ``dst[i]``, for every i,
     or for i below ``num_pairs[0]`` (an int32 tensor on the device)."""
-    dev = k_cache.device
-    _check_caches(k_cache, v_cache)
-    _expect("src", src, torch.int32, (None,), dev)
-    _expect("dst", dst, torch.int32, src.shape, dev)
+    index, kdt = k_cache.get_device(), k_cache.dtype
+    cache, pairs = _sizes("k_cache", k_cache, 4), _sizes("src", src, 1)
+    n = None
     if num_pairs is not None:
-        _expect("num_pairs", num_pairs, torch.int32, (None,), dev)
-        if num_pairs.shape[0] < 1:
+        (count,) = _sizes("num_pairs", num_pairs, 1)
+        if count < 1:
             raise ValueError("num_pairs is empty")
-    if workspace is not None:
-        _expect("workspace", workspace, torch.uint8, (None,), dev)
-    desc = make_desc(k_cache, k_cache.shape[1], 0, 1, workspace)
-    ctx, st = _on(k_cache, stream)
-    with ctx:
-        rc = cpa_copy_pages(_ptr(src), _ptr(dst), _ptr(num_pairs), src.shape[0], _ptr(k_cache),
-                            _ptr(v_cache), desc, st)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_copy_pages")
+        n = _expect("num_pairs", num_pairs, torch.int32, (count,), index)
+    at = (_expect("src", src, torch.int32, pairs, index), _expect("dst", dst, torch.int32, pairs, index),
+          n, pairs[0], _expect("k_cache", k_cache, kdt, cache, index),
+          _expect("v_cache", v_cache, kdt, cache, index))
+    desc = _cache_desc(k_cache, cache[1], 0, 1, workspace,
+                       torch.bfloat16 if kdt is torch.uint8 else kdt, 1.0, 1.0, index)
+    _launch("cpa_copy_pages", load().cpa_copy_pages, index, stream, at, desc, False)
 
 
 def fork_sequences(parents, children, block_table, seq_lens, page_refs, workspace,
                    stream=None) -> None:
     """Row ``children[i]`` becomes a copy of row ``parents[i]`` that shares its pages."""
-    desc = _pool_desc(block_table, page_refs, workspace)
-    dev = page_refs.device
-    _expect("parents", parents, torch.int32, (None,), dev)
-    _expect("children", children, torch.int32, parents.shape, dev)
-    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
-    ctx, st = _on(page_refs, stream)
-    with ctx:
-        rc = cpa_fork_sequences(_ptr(parents), _ptr(children), parents.shape[0], _ptr(block_table),
-                                _ptr(seq_lens), block_table.shape[0], _ptr(page_refs), desc, st)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_fork_sequences")
+    index, rows, table, refs, desc = _pool(block_table, page_refs, workspace)
+    n = _sizes("parents", parents, 1)
+    at = (_expect("parents", parents, torch.int32, n, index),
+          _expect("children", children, torch.int32, n, index), n[0], table,
+          _expect("seq_lens", seq_lens, torch.int32, (rows,), index), rows, refs)
+    _launch("cpa_fork_sequences", load().cpa_fork_sequences, index, stream, at, desc, False)
 
 
 def extend_sequences(query_start_loc, seq_lens, block_table, page_refs, slot_mapping, copy_src,
@@ -487,53 +506,37 @@ def extend_sequences(query_start_loc, seq_lens, block_table, page_refs, slot_map
     """Pages, slots and copies for a step's new tokens (``seq_lens`` counts
     them): fills ``slot_mapping``, the pairs' list and ``counts`` = (pairs, pages
     taken), the latter negative where the pool has too few."""
-    desc = _pool_desc(block_table, page_refs, workspace, slot_mapping.shape[0])
-    dev, n = page_refs.device, seq_lens.shape[0]
-    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
-    _expect("query_start_loc", query_start_loc, torch.int32, (n + 1,), dev)
-    _expect("slot_mapping", slot_mapping, torch.int64, (None,), dev)
-    _expect("counts", counts, torch.int32, (2,), dev)
-    _check_pairs(copy_src, copy_dst, n, dev)
-    ctx, st = _on(page_refs, stream)
-    with ctx:
-        rc = cpa_extend_sequences(_ptr(query_start_loc), _ptr(seq_lens), n, _ptr(block_table),
-                                  _ptr(page_refs), _ptr(slot_mapping), _ptr(copy_src),
-                                  _ptr(copy_dst), _ptr(counts), desc, st)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_extend_sequences")
+    tokens = _sizes("slot_mapping", slot_mapping, 1)
+    index, rows, table, refs, desc = _pool(block_table, page_refs, workspace, tokens[0])
+    at = (_expect("query_start_loc", query_start_loc, torch.int32, (rows + 1,), index),
+          _expect("seq_lens", seq_lens, torch.int32, (rows,), index), rows, table, refs,
+          _expect("slot_mapping", slot_mapping, torch.int64, tokens, index),
+          *_pairs(copy_src, copy_dst, rows, index),
+          _expect("counts", counts, torch.int32, (2,), index))
+    _launch("cpa_extend_sequences", load().cpa_extend_sequences, index, stream, at, desc, False)
 
 
 def release_pages(rows, block_table, seq_lens, page_refs, workspace, window=0, sinks=0,
                   stream=None) -> None:
     """Gives back the pages of ``rows`` (None: all rows): every page, or, with a
     window, those that the queries to come do not see."""
-    desc = _pool_desc(block_table, page_refs, workspace)
-    dev = page_refs.device
+    index, every, table, refs, desc = _pool(block_table, page_refs, workspace)
+    n, which = every, None
     if rows is not None:
-        _expect("rows", rows, torch.int32, (None,), dev)
-    _expect("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev)
-    n = block_table.shape[0] if rows is None else rows.shape[0]
-    ctx, st = _on(page_refs, stream)
-    with ctx:
-        rc = cpa_release_pages(_ptr(rows), n, _ptr(block_table), _ptr(seq_lens),
-                               block_table.shape[0], window, sinks, _ptr(page_refs), desc, st)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_release_pages")
+        (n,) = _sizes("rows", rows, 1)
+        which = _expect("rows", rows, torch.int32, (n,), index)
+    at = (which, n, table, _expect("seq_lens", seq_lens, torch.int32, (every,), index), every, window,
+          sinks, refs)
+    _launch("cpa_release_pages", load().cpa_release_pages, index, stream, at, desc, False)
 
 
 def compact_pages(block_table, page_refs, copy_src, copy_dst, counts, workspace,
                   stream=None) -> None:
     """Packs the pool's live pages to its front: ``counts`` = (pairs to copy, live pages)."""
-    desc = _pool_desc(block_table, page_refs, workspace)
-    dev = page_refs.device
-    _expect("counts", counts, torch.int32, (2,), dev)
-    _check_pairs(copy_src, copy_dst, page_refs.shape[0] // 2, dev)
-    ctx, st = _on(page_refs, stream)
-    with ctx:
-        rc = cpa_compact_pages(_ptr(block_table), block_table.shape[0], _ptr(page_refs),
-                               _ptr(copy_src), _ptr(copy_dst), _ptr(counts), desc, st)
-    if rc != CPA_OK:
-        raise CpaError(rc, "cpa_compact_pages")
+    index, rows, table, refs, desc = _pool(block_table, page_refs, workspace)
+    at = (table, rows, refs, *_pairs(copy_src, copy_dst, page_refs.shape[0] // 2, index),
+          _expect("counts", counts, torch.int32, (2,), index))
+    _launch("cpa_compact_pages", load().cpa_compact_pages, index, stream, at, desc, False)
 
 
 def device_status(k_cache, num_q_heads, max_pages_per_seq, workspace, stream=None) -> int:
