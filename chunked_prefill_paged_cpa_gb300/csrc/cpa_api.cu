@@ -227,6 +227,16 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     if (clear_bytes > desc->workspace_bytes) return CPA_ERR_WORKSPACE;
     if (cudaMemsetAsync(desc->workspace, 0, clear_bytes, st) != cudaSuccess) return CPA_ERR_CUDA;
   }
+  if (w.step && win.window && p.num_tokens == num_seqs) {
+    // every sequence has one token
+    if (nr.k && launch_kv_append(nr.k, nr.v, nr.slots, const_cast<void *>(k_cache),
+                                 const_cast<void *>(v_cache), desc->num_tokens, p.Hkv, p.D,
+                                 p.page_size, p.num_pages, 2,
+                                 p.kv_e4m3 ? (p.act_f16 ? 2 : 1) : 0, p.k_scale, p.v_scale,
+                                 p.status, st) != cudaSuccess)
+      return CPA_ERR_CUDA;
+    return launch_window_decode(p, grid, st) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+  }
   if (w.step) {
     // One launch pair for the whole step: the plan (with the append when it
     // is fused into the call), then the persistent step kernel.

@@ -149,6 +149,10 @@ cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t s
 // (attn_chunk_tf32.cu); the decode rows then go to the row kernel (rows_mode 2).
 cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
 
+// A windowed step of single tokens with 16-bit queries (attn_window_decode.cu),
+// the new rows already in the cache.
+cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream);
+
 // Checks of the cache's shape shared by the calls (cpa_api.cu).
 int check_shape(const cpa_desc *d);
 

@@ -181,3 +181,95 @@ def test_on_another_stream(cuda_device):
                                        b["scale"], ws, 60, 4, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+# ---- steps of single tokens alone
+
+TOKENS = [1, 2, 15, 16, 17, 40, 130, 700, 2049, 4000]
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_single_tokens(cuda_device, mode, window, sinks):
+    b = make_batch([1] * len(TOKENS), TOKENS, 8, 2, 128, mode, window, sinks, 60 + window, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{mode} {window} {sinks}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (6, 3), (4, 1), (8, 1), (32, 8), (16, 2)])
+def test_single_tokens_heads(cuda_device, mode, d, hq, hkv):
+    b = make_batch([1] * 3, [333, 5, 1500], hq, hkv, d, mode, 400, 5, 510 + hq, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{mode} {hq}/{hkv} {d}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_single_tokens_appended(cuda_device, mode):
+    b = make_batch([1] * len(TOKENS), TOKENS, 8, 2, 64, mode, 150, 4, 31, cuda_device)
+    whole = [b["k_cache"].clone(), b["v_cache"].clone()]
+    page, off = b["slots"] // 16, b["slots"] % 16
+    for c in ("k_cache", "v_cache"):
+        b[c][page, :, off] = 0x7F if b[c].dtype == torch.uint8 else float("nan")
+    check(b, window_call(b, workspace(b), append=True), mode)
+    for got, want in zip((b["k_cache"], b["v_cache"]), whole):
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "f16-e4m3"])
+@pytest.mark.parametrize("seqs", [1, 7, 500])
+def test_single_tokens_far_into_their_sequences(cuda_device, mode, seqs):
+    g = torch.Generator().manual_seed(seqs)
+    lens = torch.randint(1, 60_000 if seqs < 100 else 3000, (seqs,), generator=g).tolist()
+    b = make_batch([1] * seqs, lens, 4, 1, 64, mode, 1800, 20, 7, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), mode)
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "bf16-e4m3"])
+def test_single_tokens_captured_and_replayed(cuda_device, mode):
+    b = make_batch([1] * len(TOKENS), TOKENS, 8, 2, 64, mode, 60, 4, 41, cuda_device)
+    ws, out = workspace(b), torch.empty_like(b["q"])
+    eager = window_call(b, ws, append=True).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        window_call(b, ws, append=True, out=out)
+    for _ in range(2):
+        out.zero_()
+        ws[256:].random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "bf16-e4m3"])
+def test_single_tokens_a_bad_page_is_reported(cuda_device, mode):
+    """... and the other rows are right."""
+    b = make_batch([1, 1, 1], [300, 300, 300], 4, 2, 64, mode, 50, 4, 5, cuda_device)
+    ws, good = workspace(b), None
+    good = window_call(b, ws).clone()
+    b["table"][1, 300 // 16] = -5
+    got = window_call(b, ws)
+    assert status(b, ws) == ops.CPA_ERR_DEVICE
+    assert torch.equal(got[0], good[0]) and torch.equal(got[2], good[2])
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32"])
+def test_the_same_sequence_twice_in_one_step(cuda_device, mode):
+    """Two tokens of one sequence as two rows of the batch: both are appended before either is computed."""
+    b = make_batch([1, 1], [100, 101], 4, 2, 64, mode, 30, 4, 6, cuda_device, poison=False)
+    b["table"][0] = b["table"][1]
+    b["dense"][0] = [x[:100] for x in b["dense"][1]]
+    kv = [x.to(b["q"].dtype) for x in b["dense"][1]]
+    b["k"], b["v"] = kv[0][99:101].contiguous(), kv[1][99:101].contiguous()
+    b["slots"][0] = int(b["table"][1, 99 // 16]) * 16 + 99 % 16
+    page, off = b["slots"] // 16, b["slots"] % 16
+    b["k_cache"][page, :, off] = float("nan")
+    b["v_cache"][page, :, off] = float("nan")
+    check(b, window_call(b, workspace(b), append=True), mode)
