@@ -62,7 +62,7 @@ __device__ __forceinline__ int owner_seq(const int32_t *qsl, int num_seqs, int t
   return lo;
 }
 
-template <typename Elem, int D, int G, bool WIN>
+template <typename Elem, int D, int G>
 __global__ void __launch_bounds__(kWarps * 32)
 attn_rows_kernel(const AttnParams p) {
   constexpr int DL = D / 32;
@@ -80,16 +80,8 @@ attn_rows_kernel(const AttnParams p) {
     if (threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_PAGE);
     ctx = cap;
   }
-  int vis = ctx - q_len + (t - qs) + 1;
+  const int vis = ctx - q_len + (t - qs) + 1;
   if (vis <= 0) return;  // malformed row (q_len > ctx); host contract forbids it
-  // With a window the row sees [0, near) and [far, vis): numbered through both
-  // runs, the splits are those of a shorter context.
-  int near = 0, far = 0;
-  if (WIN) {
-    far = max(0, vis - p.window);
-    near = min(p.sinks, far);
-    vis -= far - near;
-  }
   int nsplit = 1;
   if (q_len == 1) {
     nsplit = (vis + kSplitKeys - 1) / kSplitKeys;
@@ -122,8 +114,7 @@ attn_rows_kernel(const AttnParams p) {
     for (int e = 0; e < DL; ++e) o[gh][e] = 0.f;
   }
 
-  for (int i = k0 + warp; i < k1; i += kWarps) {
-    const int j = WIN && i >= near ? i + (far - near) : i;
+  for (int j = k0 + warp; j < k1; j += kWarps) {
     const int page = __ldg(bt + j / p.page_size);
     if (page < 0 || page >= p.num_pages) {
       if (lane == 0) atomicOr(p.status, STATUS_BAD_PAGE);
@@ -214,14 +205,14 @@ attn_rows_kernel(const AttnParams p) {
   if (threadIdx.x == 0) p.counters[(int64_t)s * p.Hkv + g] = 0u;  // ready for next launch
 }
 
-template <typename Elem, int D, bool WIN>
+template <typename Elem, int D>
 cudaError_t launch_d(const AttnParams &p, cudaStream_t stream) {
   const dim3 grid(p.num_tokens, p.Hkv, p.rows_mode == 1 ? 1 : p.max_splits);
   switch (p.Hq / p.Hkv) {
-    case 1: attn_rows_kernel<Elem, D, 1, WIN><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case 2: attn_rows_kernel<Elem, D, 2, WIN><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case 4: attn_rows_kernel<Elem, D, 4, WIN><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case 8: attn_rows_kernel<Elem, D, 8, WIN><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case 1: attn_rows_kernel<Elem, D, 1><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case 2: attn_rows_kernel<Elem, D, 2><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case 4: attn_rows_kernel<Elem, D, 4><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case 8: attn_rows_kernel<Elem, D, 8><<<grid, kWarps * 32, 0, stream>>>(p); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
@@ -231,14 +222,11 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t stream) {
 
 cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  if (dtype == CPA_F32 && p.window) {
-    return p.D == 64 ? launch_d<float, 64, true>(p, stream) : launch_d<float, 128, true>(p, stream);
-  }
   if (dtype == CPA_F32) {
-    return p.D == 64 ? launch_d<float, 64, false>(p, stream) : launch_d<float, 128, false>(p, stream);
+    return p.D == 64 ? launch_d<float, 64>(p, stream) : launch_d<float, 128>(p, stream);
   }
-  return p.D == 64 ? launch_d<__nv_bfloat16, 64, false>(p, stream)
-                   : launch_d<__nv_bfloat16, 128, false>(p, stream);
+  return p.D == 64 ? launch_d<__nv_bfloat16, 64>(p, stream)
+                   : launch_d<__nv_bfloat16, 128>(p, stream);
 }
 
 }  // namespace cpa

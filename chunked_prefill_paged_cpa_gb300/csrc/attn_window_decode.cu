@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kPageKeys = 16;
 constexpr int kWarps = 4;
+constexpr int kMaxCluster = 8;            // (portable)
 constexpr int kHeads = 8;                 // N of the MMAs
 constexpr float kMoveThreshold = 8.0f;    // log2 units, as in the step kernel
 
@@ -382,16 +383,32 @@ cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D>, p);
 }
 
+// Pages that a row sees at most.
+int64_t page_bound(const AttnParams &p) {
+  return std::min<int64_t>(p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 1 +
+                                            (p.sinks + kPageKeys - 1) / kPageKeys);
+}
+
 }  // namespace
 
+// A cluster has at most eight CTAs: few rows with a long window leave SMs idle,
+// which the step kernel, whose splits have no such bound, does not.  Measured
+// (one token of 8 kv heads, head_dim 128, bf16; one of 1 kv head; this kernel
+// against the step kernel): window 4096 11 / 18 us and 11 / 20 us, window 16384
+// 30 / 24 and 26 / 36, window 65536 104 / 60 and 100 / 70.  Where the clusters
+// fill half the SMs or more (4 tokens of 8 kv heads, window 65536) 160 / 281 us.
+bool window_decode_takes(const AttnParams &p, int sms) {
+  const int64_t rows = (int64_t)p.num_tokens * p.Hkv;
+  return rows * kMaxCluster > sms || page_bound(p) <= 32 * kMaxCluster * kWarps;
+}
+
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream) {
-  // CTAs per (token, kv head): enough to give every SM two, as long as every
-  // warp has a page
-  const int64_t pages = std::min<int64_t>(
-      p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 1 + (p.sinks + kPageKeys - 1) / kPageKeys);
+  // CTAs per (token, kv head): as many as are resident at a time (two per SM),
+  // as long as every warp has a page
+  const int64_t pages = page_bound(p);
   const int64_t rows = (int64_t)p.num_tokens * p.Hkv;
   int nc = 1;
-  while (nc < 8 && rows * nc < 2 * sms && pages > (int64_t)nc * kWarps) nc *= 2;
+  while (nc < kMaxCluster && rows * nc <= sms && pages > (int64_t)nc * kWarps) nc *= 2;
   if (p.D == 128) {
     if (p.kv_e4m3) return launch<2, 128>(p, nc, stream);
     return p.act_f16 ? launch<1, 128>(p, nc, stream) : launch<0, 128>(p, nc, stream);

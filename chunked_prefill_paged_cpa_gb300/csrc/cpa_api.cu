@@ -213,11 +213,13 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.status = reinterpret_cast<uint32_t *>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   int grid = 0;
-  if (w.step) {
+  if (w.step || win.window) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CPA_ERR_CUDA;
     grid = std::min(sm_count(dev), kMaxStepGrid);
     if (grid <= 0) return CPA_ERR_CUDA;
+  }
+  if (w.step) {
     if (num_seqs > kDecodeMaxSeqs) return CPA_ERR_UNSUPPORTED;
     // tensor-map row coordinates and page-stream offsets are 32-bit
     if ((int64_t)p.num_pages * p.Hkv * p.page_size >= INT32_MAX) return CPA_ERR_UNSUPPORTED;
@@ -227,15 +229,17 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     if (clear_bytes > desc->workspace_bytes) return CPA_ERR_WORKSPACE;
     if (cudaMemsetAsync(desc->workspace, 0, clear_bytes, st) != cudaSuccess) return CPA_ERR_CUDA;
   }
-  if (w.step && win.window && p.num_tokens == num_seqs) {
-    // every sequence has one token
+  // with a window: fp32 steps, and steps of one token per sequence
+  const bool single = w.step && win.window && p.num_tokens == num_seqs && window_decode_takes(p, grid);
+  if (single || (win.window && !w.step)) {
     if (nr.k && launch_kv_append(nr.k, nr.v, nr.slots, const_cast<void *>(k_cache),
                                  const_cast<void *>(v_cache), desc->num_tokens, p.Hkv, p.D,
-                                 p.page_size, p.num_pages, 2,
+                                 p.page_size, p.num_pages, w.step ? 2 : 4,
                                  p.kv_e4m3 ? (p.act_f16 ? 2 : 1) : 0, p.k_scale, p.v_scale,
                                  p.status, st) != cudaSuccess)
       return CPA_ERR_CUDA;
-    return launch_window_decode(p, grid, st) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    const cudaError_t e = single ? launch_window_decode(p, grid, st) : launch_window_f32(p, grid, st);
+    return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
   }
   if (w.step) {
     // One launch pair for the whole step: the plan (with the append when it
@@ -279,7 +283,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.part_o = reinterpret_cast<float *>(ws + w.part_o);
   p.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
   p.rows_mode = 0;
-  if (desc->dtype == CPA_F32 && !win.window) {
+  if (desc->dtype == CPA_F32) {
     // the chunk rows on the tensor cores (tf32), the decode rows on the row kernel
     if (launch_chunk_tf32(p, st) != cudaSuccess) return CPA_ERR_CUDA;
     p.rows_mode = 2;

@@ -151,7 +151,11 @@ cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
 
 // A windowed step of single tokens with 16-bit queries (attn_window_decode.cu),
 // the new rows already in the cache.
+bool window_decode_takes(const AttnParams &p, int sms);
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream);
+
+// A windowed fp32 step (attn_window_f32.cu), the new rows already in the cache.
+cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream);
 
 // Checks of the cache's shape shared by the calls (cpa_api.cu).
 int check_shape(const cpa_desc *d);

@@ -215,7 +215,11 @@ int cpa_append_attention_forward(const void *q, const void *k, const void *v,
  *    chunk; a decode on its own) sees may hold anything, NaN included.  Inside
  *    a chunk a non-finite V that one row of the group sees can make the outputs
  *    of the group's other rows non-finite, as in cpa_attention_forward.
- *  - fp32 activations are computed in fp32 throughout (no tf32 products). */
+ *  - fp32 activations keep fp32's precision: the tensor cores multiply each
+ *    operand as the sum of two tf32 values, the products' error is below
+ *    2^-21 (cpa_attention_forward rounds a chunk's operands to tf32).  There a
+ *    non-finite q, K or V that a row sees gives non-finite outputs, NaN where
+ *    the formula's value is infinite. */
 int cpa_window_attention_forward(const void *q, const void *k_cache, const void *v_cache,
                                  const int32_t *block_table, const int32_t *query_start_loc,
                                  const int32_t *seq_lens, int32_t num_seqs, float scale,

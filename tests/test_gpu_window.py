@@ -273,3 +273,43 @@ def test_the_same_sequence_twice_in_one_step(cuda_device, mode):
     b["k_cache"][page, :, off] = float("nan")
     b["v_cache"][page, :, off] = float("nan")
     check(b, window_call(b, workspace(b), append=True), mode)
+
+
+# ---- fp32: tiles of few rows and of many
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (16, 2)])
+def test_f32_chunks(cuda_device, d, hq, hkv):
+    """Chunks of one row to many tiles, tails of every kind."""
+    b = make_batch([17, 1, 130, 5, 1, 64], [300, 250, 130, 77, 1, 640], hq, hkv, d, "f32", 90, 19, 70 + hq, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{hq}/{hkv} {d}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (300, 7), (5000, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_f32_many_rows(cuda_device, d, window, sinks):
+    """Enough tiles for four to a CTA (19200 rows and more of 32 heads)."""
+    b = make_batch([1, 601, 33, 3, 250, 1], [40, 700, 33, 500, 1100, 900], 32, 8, d, "f32", window, sinks, 80 + window, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), f"{d} {window} {sinks}")
+    assert status(b, ws) == ops.CPA_OK
+
+
+def test_f32_precision(cuda_device):
+    """Far closer to the formula than tf32 products could be: 2^-11 of the operands' half step against 2^-21."""
+    b = make_batch([200, 1], [900, 1000], 8, 2, 128, "f32", 700, 4, 90, cuda_device)
+    want, size = reference(b)
+    err = (window_call(b, workspace(b)).double() - want).norm() / want.norm()
+    assert err < 2.0 ** -19
+
+
+@pytest.mark.parametrize("seqs", [33, 1025, 3000])
+def test_f32_finds_its_sequence(cuda_device, seqs):
+    """Many sequences, some of several tokens."""
+    g = torch.Generator().manual_seed(seqs)
+    q = torch.where(torch.rand(seqs, generator=g) < 0.1, torch.randint(2, 20, (seqs,), generator=g), 1).tolist()
+    lens = [x + int(y) for x, y in zip(q, torch.randint(0, 60, (seqs,), generator=g))]
+    b = make_batch(q, lens, 2, 1, 64, "f32", 21, 3, 4, cuda_device)
+    check(b, window_call(b, workspace(b)))
