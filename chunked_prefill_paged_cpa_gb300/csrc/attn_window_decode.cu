@@ -12,7 +12,6 @@
 // the order of O's dims: both are chosen so that a lane's elements of a row are
 // whole 16-byte words and a warp's loads whole rows.  P turns from S's layout
 // (keys down the lanes) into an operand's (heads down the lanes) by movmatrix.
-// The next page's words are loaded before a page is computed.
 //
 // The operator is bound by HBM: 16-row tensor instructions reach a fraction of
 // the tcgen05 rate, but a page costs about 120 of a warp's instructions, and
@@ -78,7 +77,7 @@ struct PageRegs {
   uint32_t k[2][KC * 4];
   uint32_t v[4][VW];
 
-  __device__ __forceinline__ void load(const unsigned char *kp, const unsigned char *vp, int r, int c) {
+  __device__ __forceinline__ void load_k(const unsigned char *kp, int r, int c) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -89,6 +88,8 @@ struct PageRegs {
         k[h][4 * i + 2] = x.z;
         k[h][4 * i + 3] = x.w;
       }
+  }
+  __device__ __forceinline__ void load_v(const unsigned char *vp, int r, int c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const unsigned char *row = vp + (2 * c + (j & 1) + 8 * (j >> 1)) * (D * EB) + r * (VW * 4);
@@ -187,10 +188,10 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
       }
     }
   };
-  auto fetch = [&](Page &x, int v) -> int {  // page v's words; its entry
+  auto find = [&](int v, int64_t &at) -> int {  // page v's place in the caches; its entry
+    if (((v - v0) & 31) == 0) look_up(v);
     const int e = __shfl_sync(0xffffffffu, entry, (v - v0) & 31);
-    const int64_t at = (int64_t)max(e, 0) * p.Hkv * page_bytes;
-    x.load(kc + at, vc + at, r, c);
+    at = (int64_t)max(e, 0) * p.Hkv * page_bytes;
     return e;
   };
 
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c and 2c + 1
   const float sl2 = p.scale_log2;
 
-  auto compute = [&](Page &x, int v, int e) {
+  // Page v, held in x: S, then after_s(); softmax and O, then after_o().
+  auto page = [&](Page &x, int v, int e, auto after_s, auto after_o) {
     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
       }
       mma16<F16>((ks & 1) ? sb : sa, a, qb[ks][0], qb[ks][1]);
     }
+    after_s();
     float sc[4];  // (key r, heads 2c, 2c + 1), (key r + 8, the same)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = (sa[i] + sb[i]) * sl2;
@@ -283,24 +286,55 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
       }
       mma16<F16>(o[i], a, b0, b1);
     }
+    after_o();
   };
 
-  if (v0 < v1) {
-    Page a, b;
-    int ea, eb = -1;
-    look_up(v0);
-    ea = fetch(a, v0);
-    for (int v = v0; v < v1; v += 2) {
-      // (32 entries at a time: a refill falls between an odd page and an even one)
-      if (v + 1 < v1) eb = fetch(b, v + 1);
-      compute(a, v, ea);
-      if (v + 1 < v1) {
-        if (v + 2 < v1) {
-          if (((v + 2 - v0) & 31) == 0) look_up(v + 2);
-          ea = fetch(a, v + 2);
+  // The next page is on its way while a page is computed.  16-bit caches: into
+  // a second set of registers.  8-bit caches, whose pages are half as long:
+  // K's words as soon as S has used K's registers, V's after O has used V's; the
+  // registers saved hold a third more warps.  (256 and 64 tokens of 8 kv heads,
+  // window 4096, head_dim 128: bf16 612 / 163 us with a second set, 619 / 206
+  // without; E4M3 337 / 120 and 341 / 87 us.)
+  if constexpr (KVM != 2) {
+    auto none = [] {};
+    auto fetch = [&](Page &x, int v) {
+      int64_t at;
+      const int e = find(v, at);
+      x.load_k(kc + at, r, c);
+      x.load_v(vc + at, r, c);
+      return e;
+    };
+    if (v0 < v1) {
+      Page a, b;
+      int ea = fetch(a, v0), eb = -1;
+      for (int v = v0; v < v1; v += 2) {
+        if (v + 1 < v1) eb = fetch(b, v + 1);
+        page(a, v, ea, none, none);
+        if (v + 1 < v1) {
+          if (v + 2 < v1) ea = fetch(a, v + 2);
+          page(b, v + 1, eb, none, none);
         }
-        compute(b, v + 1, eb);
       }
+    }
+  } else if (v0 < v1) {
+    Page x;
+    int64_t at;
+    int e = find(v0, at), next = -1;
+    x.load_k(kc + at, r, c);
+    x.load_v(vc + at, r, c);
+    for (int v = v0; v < v1; ++v) {
+      const bool more = v + 1 < v1;
+      page(x, v, e,
+           [&] {
+             if (more) {
+               next = find(v + 1, at);
+               x.load_k(kc + at, r, c);
+             }
+           },
+           [&] {
+             if (more) x.load_v(vc + at, r, c);
+           });
+      e = next;
     }
   }
 
@@ -368,8 +402,35 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
+// Pages that a row sees at most.
+int64_t page_bound(const AttnParams &p) {
+  return std::min<int64_t>(p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 1 +
+                                            (p.sinks + kPageKeys - 1) / kPageKeys);
+}
+
 template <int KVM, int D>
-cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
+  // CTAs per (token, kv head): the number with the fewest rounds of resident
+  // CTAs, counted in a warp's pages, a start and a join costing about three
+  static const int resident = [] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D>, kWarps * 32, 0) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return std::max(n, 1);
+  }();
+  const int64_t rows = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)resident * sms, pages = page_bound(p);
+  int nc = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= kMaxCluster; n *= 2) {
+    const int64_t cost = (rows * n + slots - 1) / slots * ((pages + n * kWarps - 1) / (n * kWarps) + 3);
+    if (cost < least) {
+      least = cost;
+      nc = n;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc, p.Hkv, p.num_tokens);
   cfg.blockDim = dim3(kWarps * 32);
@@ -381,12 +442,6 @@ cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D>, p);
-}
-
-// Pages that a row sees at most.
-int64_t page_bound(const AttnParams &p) {
-  return std::min<int64_t>(p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 1 +
-                                            (p.sinks + kPageKeys - 1) / kPageKeys);
 }
 
 }  // namespace
@@ -403,18 +458,12 @@ bool window_decode_takes(const AttnParams &p, int sms) {
 }
 
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream) {
-  // CTAs per (token, kv head): as many as are resident at a time (two per SM),
-  // as long as every warp has a page
-  const int64_t pages = page_bound(p);
-  const int64_t rows = (int64_t)p.num_tokens * p.Hkv;
-  int nc = 1;
-  while (nc < kMaxCluster && rows * nc <= sms && pages > (int64_t)nc * kWarps) nc *= 2;
   if (p.D == 128) {
-    if (p.kv_e4m3) return launch<2, 128>(p, nc, stream);
-    return p.act_f16 ? launch<1, 128>(p, nc, stream) : launch<0, 128>(p, nc, stream);
+    if (p.kv_e4m3) return launch<2, 128>(p, sms, stream);
+    return p.act_f16 ? launch<1, 128>(p, sms, stream) : launch<0, 128>(p, sms, stream);
   }
-  if (p.kv_e4m3) return launch<2, 64>(p, nc, stream);
-  return p.act_f16 ? launch<1, 64>(p, nc, stream) : launch<0, 64>(p, nc, stream);
+  if (p.kv_e4m3) return launch<2, 64>(p, sms, stream);
+  return p.act_f16 ? launch<1, 64>(p, sms, stream) : launch<0, 64>(p, sms, stream);
 }
 
 }  // namespace cpa

@@ -214,6 +214,13 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
   __shared__ int64_t warps[32];
   __shared__ int found[2];  // free pages in this CTA's piece, by turn
 
+  // the first turn's references, on their way while the rows are looked at
+  const int64_t first = ((int64_t)rank * kExtThreads + tid) * kExtPages;
+  const bool whole = first + kExtPages <= a.num_pages;
+  int4 head_refs[kExtPages / 4];
+#pragma unroll
+  for (int i = 0; i < kExtPages / 4; ++i)
+    head_refs[i] = whole ? *reinterpret_cast<const int4 *>(a.refs + first + 4 * i) : make_int4(1, 1, 1, 1);
   for (int i = tid; i < H; i += kExtThreads) {
     h_page[i] = -1;
     h_count[i] = 0;
@@ -298,7 +305,8 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
   }
   const int needed = (int)(sum & 0xffffffff), copies = (int)(sum >> 32);
 
-  // B: the lowest free pages, in turns of 16 K pages per CTA
+  // B: the lowest free pages, in turns of 16 K pages per CTA (skipped where
+  // nothing is needed)
   int64_t have = 0;
   int turn = 0;
   for (int64_t p0 = 0; p0 < a.num_pages && have < needed; p0 += (int64_t)nb * kExtThreads * kExtPages, ++turn) {
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
     if (p + kExtPages <= a.num_pages) {
 #pragma unroll
       for (int i = 0; i < kExtPages / 4; ++i) {
-        const int4 r = *reinterpret_cast<const int4 *>(a.refs + p + 4 * i);
+        const int4 r = turn ? *reinterpret_cast<const int4 *>(a.refs + p + 4 * i) : head_refs[i];
         zero |= ((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << (4 * i);
       }
     } else {
@@ -646,14 +654,18 @@ extern "C" int cpa_extend_sequences(const int32_t *query_start_loc, const int32_
   if (cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)extend_smem(kDecodeMaxSeqs, 13)) != cudaSuccess)
     return CPA_ERR_CUDA;
+  // A CTA for every 16 K pages of the pool (one turn of the search) and every
+  // 4 K tokens, at most eight, the largest portable cluster.
+  const int64_t want = std::max((desc->num_pages + 16383) / 16384, (desc->num_tokens + 4095) / 4096);
+  const int nb = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(8);
+  cfg.gridDim = dim3(nb);
   cfg.blockDim = dim3(kExtThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 8;
+  attr[0].val.clusterDim.x = nb;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

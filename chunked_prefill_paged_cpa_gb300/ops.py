@@ -363,11 +363,15 @@ def _expect(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> int:
     raise ValueError(f"{name} is not contiguous")
 
 
-def _sizes(name: str, t: torch.Tensor, dims: int) -> torch.Size:
+def _expect_any(name: str, t: torch.Tensor, dtype, dims: int, index: int):
+    """The same for a tensor of any size: (address, shape)."""
     shape = t.shape
+    if (t.dtype is dtype and t.get_device() == index >= 0 and len(shape) == dims
+            and t.is_contiguous()):
+        return t.data_ptr(), shape
     if len(shape) != dims:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected {dims} dimensions")
-    return shape
+    return _expect(name, t, dtype, shape, index), shape
 
 
 _DTYPES = {torch.float32: CPA_F32, torch.bfloat16: CPA_BF16, torch.float16: CPA_F16}
@@ -379,8 +383,7 @@ def _cache_desc(k_cache, num_q_heads, num_tokens, max_pages, workspace, dtype, k
     num_pages, hkv, page, d = k_cache.shape
     ws = nb = 0
     if workspace is not None:
-        nb = _sizes("workspace", workspace, 1)[0]
-        ws = _expect("workspace", workspace, torch.uint8, (nb,), index)
+        ws, (nb,) = _expect_any("workspace", workspace, torch.uint8, 1, index)
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
@@ -398,16 +401,16 @@ def _window_step(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, wo
     kdt = k_cache.dtype
     if kdt is not torch.uint8 and kdt is not dt:
         raise TypeError(f"q is {dt}, the caches are {kdt}")
-    cache = _sizes("k_cache", k_cache, 4)
-    tokens, heads, _ = _sizes("q", q, 3)
-    seqs, cols = _sizes("block_table", block_table, 2)
-    qs = (tokens, heads, cache[3])
+    i32 = torch.int32
+    kc, cache = _expect_any("k_cache", k_cache, kdt, 4, index)
+    qa, qs = _expect_any("q", q, dt, 3, index)
+    table, (seqs, cols) = _expect_any("block_table", block_table, i32, 2, index)
+    tokens, heads, d = qs
+    if d != cache[3]:
+        raise ValueError(f"q has head_dim {d}, the caches have {cache[3]}")
     if out is None:
         out = torch.empty_like(q)
-    i32 = torch.int32
-    at = (_expect("q", q, dt, qs, index), _expect("k_cache", k_cache, kdt, cache, index),
-          _expect("v_cache", v_cache, kdt, cache, index),
-          _expect("block_table", block_table, i32, (seqs, cols), index),
+    at = (qa, kc, _expect("v_cache", v_cache, kdt, cache, index), table,
           _expect("query_start_loc", query_start_loc, i32, (seqs + 1,), index),
           _expect("seq_lens", seq_lens, i32, (seqs,), index), seqs)
     desc = _cache_desc(k_cache, heads, tokens, cols, workspace, dt, k_scale, v_scale, index)
@@ -450,40 +453,37 @@ def pages_workspace_for(num_pages: int, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _pool(block_table, page_refs, workspace, num_tokens: int = 0):
+def _pool(block_table, page_refs, workspace):
     """Checks of the tensors every table operator takes: (device, rows,
     addresses of the table and the references, descriptor)."""
-    index = page_refs.get_device()
-    (pages,), (rows, cols) = _sizes("page_refs", page_refs, 1), _sizes("block_table", block_table, 2)
-    nb = _sizes("workspace", workspace, 1)[0]
-    refs = _expect("page_refs", page_refs, torch.int32, (pages,), index)
-    table = _expect("block_table", block_table, torch.int32, (rows, cols), index)
-    ws = _expect("workspace", workspace, torch.uint8, (nb,), index)
-    return index, rows, table, refs, CpaDesc(1, 1, 64, 16, pages, cols, CPA_BF16, num_tokens, ws, nb,
+    index, i32 = page_refs.get_device(), torch.int32
+    refs, (pages,) = _expect_any("page_refs", page_refs, i32, 1, index)
+    table, (rows, cols) = _expect_any("block_table", block_table, i32, 2, index)
+    ws, (nb,) = _expect_any("workspace", workspace, torch.uint8, 1, index)
+    return index, rows, table, refs, CpaDesc(1, 1, 64, 16, pages, cols, CPA_BF16, 0, ws, nb,
                                              CPA_KV_SAME, 0.0, 0.0)
 
 
 def _pairs(src, dst, least: int, index: int) -> tuple:
-    ns, nd = _sizes("copy_src", src, 1)[0], _sizes("copy_dst", dst, 1)[0]
-    if min(ns, nd) < least:
-        raise ValueError(f"copy_src and copy_dst need {least} entries, they have {ns} and {nd}")
-    return (_expect("copy_src", src, torch.int32, (ns,), index),
-            _expect("copy_dst", dst, torch.int32, (nd,), index))
+    a, (na,) = _expect_any("copy_src", src, torch.int32, 1, index)
+    b, (nb,) = _expect_any("copy_dst", dst, torch.int32, 1, index)
+    if na < least or nb < least:
+        raise ValueError(f"copy_src and copy_dst need {least} entries, they have {na} and {nb}")
+    return a, b
 
 
 def copy_pages(src, dst, k_cache, v_cache, num_pairs=None, workspace=None, stream=None) -> None:
     """Copies pages ``src[i]`` of both caches to pages ``dst[i]``, for every i,
     or for i below ``num_pairs[0]`` (an int32 tensor on the device)."""
     index, kdt = k_cache.get_device(), k_cache.dtype
-    cache, pairs = _sizes("k_cache", k_cache, 4), _sizes("src", src, 1)
+    kc, cache = _expect_any("k_cache", k_cache, kdt, 4, index)
+    a, pairs = _expect_any("src", src, torch.int32, 1, index)
     n = None
     if num_pairs is not None:
-        (count,) = _sizes("num_pairs", num_pairs, 1)
+        n, (count,) = _expect_any("num_pairs", num_pairs, torch.int32, 1, index)
         if count < 1:
             raise ValueError("num_pairs is empty")
-        n = _expect("num_pairs", num_pairs, torch.int32, (count,), index)
-    at = (_expect("src", src, torch.int32, pairs, index), _expect("dst", dst, torch.int32, pairs, index),
-          n, pairs[0], _expect("k_cache", k_cache, kdt, cache, index),
+    at = (a, _expect("dst", dst, torch.int32, pairs, index), n, pairs[0], kc,
           _expect("v_cache", v_cache, kdt, cache, index))
     desc = _cache_desc(k_cache, cache[1], 0, 1, workspace,
                        torch.bfloat16 if kdt is torch.uint8 else kdt, 1.0, 1.0, index)
@@ -494,8 +494,8 @@ def fork_sequences(parents, children, block_table, seq_lens, page_refs, workspac
                    stream=None) -> None:
     """Row ``children[i]`` becomes a copy of row ``parents[i]`` that shares its pages."""
     index, rows, table, refs, desc = _pool(block_table, page_refs, workspace)
-    n = _sizes("parents", parents, 1)
-    at = (_expect("parents", parents, torch.int32, n, index),
+    a, n = _expect_any("parents", parents, torch.int32, 1, index)
+    at = (a,
           _expect("children", children, torch.int32, n, index), n[0], table,
           _expect("seq_lens", seq_lens, torch.int32, (rows,), index), rows, refs)
     _launch("cpa_fork_sequences", load().cpa_fork_sequences, index, stream, at, desc, False)
@@ -506,12 +506,11 @@ def extend_sequences(query_start_loc, seq_lens, block_table, page_refs, slot_map
     """Pages, slots and copies for a step's new tokens (``seq_lens`` counts
     them): fills ``slot_mapping``, the pairs' list and ``counts`` = (pairs, pages
     taken), the latter negative where the pool has too few."""
-    tokens = _sizes("slot_mapping", slot_mapping, 1)
-    index, rows, table, refs, desc = _pool(block_table, page_refs, workspace, tokens[0])
+    index, rows, table, refs, desc = _pool(block_table, page_refs, workspace)
+    slots, (desc.num_tokens,) = _expect_any("slot_mapping", slot_mapping, torch.int64, 1, index)
     at = (_expect("query_start_loc", query_start_loc, torch.int32, (rows + 1,), index),
           _expect("seq_lens", seq_lens, torch.int32, (rows,), index), rows, table, refs,
-          _expect("slot_mapping", slot_mapping, torch.int64, tokens, index),
-          *_pairs(copy_src, copy_dst, rows, index),
+          slots, *_pairs(copy_src, copy_dst, rows, index),
           _expect("counts", counts, torch.int32, (2,), index))
     _launch("cpa_extend_sequences", load().cpa_extend_sequences, index, stream, at, desc, False)
 
@@ -523,8 +522,7 @@ def release_pages(rows, block_table, seq_lens, page_refs, workspace, window=0, s
     index, every, table, refs, desc = _pool(block_table, page_refs, workspace)
     n, which = every, None
     if rows is not None:
-        (n,) = _sizes("rows", rows, 1)
-        which = _expect("rows", rows, torch.int32, (n,), index)
+        which, (n,) = _expect_any("rows", rows, torch.int32, 1, index)
     at = (which, n, table, _expect("seq_lens", seq_lens, torch.int32, (every,), index), every, window,
           sinks, refs)
     _launch("cpa_release_pages", load().cpa_release_pages, index, stream, at, desc, False)
