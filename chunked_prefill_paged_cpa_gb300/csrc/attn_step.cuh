@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   long long pages = 0, pairs = 0, ctiles = 0;
   for (int s = tid; s < S; s += kPlanWorkers) {
     const int qs = __ldg(p.query_start_loc + s);
-    const int q_len = __ldg(p.query_start_loc + s + 1) - qs;
+    int q_len = __ldg(p.query_start_loc + s + 1) - qs;
+    // single tokens that a kernel of their own computes beside this one
+    if (WIN && q_len == 1 && p.rows_mode == 1) q_len = 0;
     const int ctx = q_len < 1 ? 0 : seq_ctx(p, s, q_len);
     sq_qs[s] = qs;
     sq_len[s] = q_len;
@@ -748,6 +750,9 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
   const uint32_t tmem = bs->tmem_base;  // S_i at columns 128*i, O_i at 256 + 128*i
   // everything below reads what the plan kernel wrote
   ptx::grid_dependency_wait();
+  // (a kernel launched behind this one, for the single tokens, may take the SMs
+  // that this grid leaves)
+  if (WIN) ptx::grid_launch_dependents();
   const int n_items = __ldcg(w.hdr + 2);
 
   if (warp == kProducerWarp) {

@@ -69,6 +69,8 @@ __device__ __forceinline__ uint2 load8(const unsigned char *p) {
 // One page of K and V of one kv head as a lane holds it.  With r = lane / 4 and
 // c = lane % 4: of K, rows r and r + 8, 16 bytes of each 64 (at 16 c); of V,
 // rows 2c, 2c + 1, 2c + 8 and 2c + 9, the dims r D / 8 .. (r + 1) D / 8 - 1.
+// (Of V in 16 bits a lane could take 16 bytes of each 128 instead, so that every
+// load reads whole lines: measured 1.5 % slower.)
 template <int KVM, int D>
 struct PageRegs {
   static constexpr int EB = KVM == 2 ? 1 : 2;
@@ -118,21 +120,33 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   constexpr int KS = D / 16;   // k-steps of S, and 16-dim tiles of O^T
   using Page = PageRegs<KVM, D>;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = blockIdx.x, nc = gridDim.x, g = blockIdx.y, t = blockIdx.z;
+  const int rank = blockIdx.x, nc = gridDim.x, g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int G = p.Hq / p.Hkv;
 
-  // the token's sequence: t itself when every sequence has one token
-  int s = t;
-  if (t >= p.num_seqs || __ldg(p.query_start_loc + t) != t || __ldg(p.query_start_loc + t + 1) != t + 1) {
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(p.query_start_loc + mid) <= t) lo = mid; else hi = mid - 1;
+  // blockIdx.z is the token, or the sequence in a step that has chunks too
+  int t = blockIdx.z, s = t, qs, q_len;
+  if (p.rows_mode == 2) {
+    qs = __ldg(p.query_start_loc + s);
+    q_len = __ldg(p.query_start_loc + s + 1) - qs;
+    if (q_len != 1 || qs < 0 || qs >= p.num_tokens) {
+      ptx::grid_dependency_wait();
+      return;  // (the whole cluster)
     }
-    s = lo;
+    t = qs;
+  } else {
+    // the token's sequence: t itself when every sequence has one token
+    if (t >= p.num_seqs || __ldg(p.query_start_loc + t) != t || __ldg(p.query_start_loc + t + 1) != t + 1) {
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(p.query_start_loc + mid) <= t) lo = mid; else hi = mid - 1;
+      }
+      s = lo;
+    }
+    qs = __ldg(p.query_start_loc + s);
+    q_len = __ldg(p.query_start_loc + s + 1) - qs;
   }
-  const int qs = __ldg(p.query_start_loc + s), q_len = __ldg(p.query_start_loc + s + 1) - qs;
   int ctx = __ldg(p.seq_lens + s);
   const int cap = p.max_pages * kPageKeys;
   if (ctx > cap) {
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
     l1 += p1 + p3;
     const uint32_t b0 = transpose8(F16 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1));
     const uint32_t b1 = transpose8(F16 ? ptx::pack_f16x2(p2, p3) : ptx::pack_bf16x2(p2, p3));
-    // O^T tile i: dims 2i and 2i + 1 of the lane's run of dims (rows r and r + 8)
+    // O^T tile i: dims 2i and 2i + 1 of those that the lane holds (rows r and r + 8)
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       uint32_t a[4];
@@ -384,6 +398,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   };
   if (nc == 1) {
     for (int i = threadIdx.x; i < G * D; i += kWarps * 32) store(i / D, i % D, of_warps(i / D, i % D));
+    ptx::grid_dependency_wait();
     return;
   }
   __shared__ float cl_o[kHeads][D];
@@ -400,6 +415,9 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
                      [&](int b) { return *cluster.map_shared_rank(&cl_o[h][d], b); }));
   }
   cluster.sync();  // no CTA leaves while another reads its shared memory
+  // Behind a step kernel (rows_mode 2) this grid starts before that one has
+  // ended, but ends after it: what comes next on the stream sees both.
+  ptx::grid_dependency_wait();
 }
 
 // Pages that a row sees at most.
@@ -414,6 +432,13 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
   // CTAs, counted in a warp's pages, a start and a join costing about three
   static const int resident = [] {
     int n = 0;
+    // The words on their way sit in L1: an SM that the step kernel has left comes
+    // with nearly all of it as shared memory, and is to be set up anew.  (64
+    // tokens of window 4096 beside a 480-token chunk, 8-bit cache: 192 us without
+    // this hint, 151 us with it.)
+    if (cudaFuncSetAttribute(window_decode_kernel<KVM, D>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout, 40) != cudaSuccess)
+      cudaGetLastError();
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D>, kWarps * 32, 0) !=
         cudaSuccess) {
       cudaGetLastError();
@@ -421,7 +446,7 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
     }
     return std::max(n, 1);
   }();
-  const int64_t rows = (int64_t)p.num_tokens * p.Hkv, slots = (int64_t)resident * sms, pages = page_bound(p);
+  const int64_t rows = (int64_t)(p.rows_mode == 2 ? p.num_seqs : p.num_tokens) * p.Hkv, slots = (int64_t)resident * sms, pages = page_bound(p);
   int nc = 1;
   int64_t least = INT64_MAX;
   for (int n = 1; n <= kMaxCluster; n *= 2) {
@@ -432,15 +457,17 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nc, p.Hkv, p.num_tokens);
+  cfg.gridDim = dim3(nc, p.Hkv, p.rows_mode == 2 ? p.num_seqs : p.num_tokens);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = nc;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.rows_mode == 2 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D>, p);
 }
 
@@ -455,6 +482,20 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
 bool window_decode_takes(const AttnParams &p, int sms) {
   const int64_t rows = (int64_t)p.num_tokens * p.Hkv;
   return rows * kMaxCluster > sms || page_bound(p) <= 32 * kMaxCluster * kWarps;
+}
+
+// Mixed steps: over an 8-bit cache the step kernel spends more on widening a
+// decode's pages than HBM on reading them, and the single tokens are better
+// computed here, on the SMs that the chunks leave, once they are enough to pay
+// for two more launches.  Measured (this kernel beside the step kernel against
+// the step kernel alone, window 1024, a 480-token chunk, 8 kv heads): 16 tokens
+// 48 / 48 us, 32 tokens (111 pages per SM) 54 / 64, 64 tokens 60 / 93; window 4096
+// and 16 tokens 104 / 134.  16-bit caches gain little (64 tokens 78 / 82 us) and
+// lose it again on a cold start: they stay in the step kernel's queue.
+bool window_decode_beside(const AttnParams &p, int sms) {
+  constexpr int kLeastPages = 96;  // per SM
+  return p.kv_e4m3 && window_decode_takes(p, sms) &&
+         (int64_t)p.num_seqs * p.Hkv * page_bound(p) >= (int64_t)kLeastPages * sms;
 }
 
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream) {

@@ -58,7 +58,7 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
 
 // Eight keys of K and V of one kv head as a lane holds them.  With r = lane / 4
 // and c = lane % 4: of K, row r, 16 bytes of each 64 (at 16 c); of V, rows 2c
-// and 2c + 1, the dims r D / 8 .. (r + 1) D / 8 - 1.
+// and 2c + 1, 16 bytes of each 128 (at 16 r).
 template <int D>
 struct UnitRegs {
   float k[D / 4];
@@ -79,7 +79,7 @@ struct UnitRegs {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(vp + (2 * c + j) * D + r * (D / 8) + i * 4));
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(vp + (2 * c + j) * D + i * 32 + r * 4));
         v[j][4 * i] = x.x;
         v[j][4 * i + 1] = x.y;
         v[j][4 * i + 2] = x.z;
@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     la += __shfl_xor_sync(0xffffffffu, la, k);
     lb += __shfl_xor_sync(0xffffffffu, lb, k);
   }
-  // O tile i: column n stands for dim n D / 8 + i; this lane has columns 2c and 2c + 1
+  // O tile i: column n stands for dim i / 4 * 32 + 4 n + i % 4; this lane has
+  // columns 2c and 2c + 1
   auto row_out = [&](int tok, int row) {
     return static_cast<float *>(p.out) + ((int64_t)(qs + tok) * p.Hq + g * G + row % G) * D;
   };
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int i = 0; i < KS; i += 4)
-          *reinterpret_cast<float4 *>(to + (2 * c + n) * (D / 8) + i) =
+          *reinterpret_cast<float4 *>(to + i * 8 + (2 * c + n) * 4) =
               make_float4(o[i][2 * h + n] / l, o[i + 1][2 * h + n] / l, o[i + 2][2 * h + n] / l,
                           o[i + 3][2 * h + n] / l);
     }
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < KS; i += 4)
-        *reinterpret_cast<float4 *>(sm_o + (warp * kRows + r + 8 * h) * D + (2 * c + n) * (D / 8) + i) =
+        *reinterpret_cast<float4 *>(sm_o + (warp * kRows + r + 8 * h) * D + i * 8 + (2 * c + n) * 4) =
             make_float4(o[i][2 * h + n], o[i + 1][2 * h + n], o[i + 2][2 * h + n], o[i + 3][2 * h + n]);
   __syncthreads();
   struct State {

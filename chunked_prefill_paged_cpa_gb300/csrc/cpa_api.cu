@@ -231,15 +231,21 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   }
   // with a window: fp32 steps, and steps of one token per sequence
   const bool single = w.step && win.window && p.num_tokens == num_seqs && window_decode_takes(p, grid);
-  if (single || (win.window && !w.step)) {
+  // a mixed step's single tokens beside the step kernel of its chunks
+  const bool beside = w.step && win.window && p.num_tokens > num_seqs && num_seqs > 1 &&
+                      window_decode_beside(p, grid);
+  if (single || beside || (win.window && !w.step)) {
     if (nr.k && launch_kv_append(nr.k, nr.v, nr.slots, const_cast<void *>(k_cache),
                                  const_cast<void *>(v_cache), desc->num_tokens, p.Hkv, p.D,
                                  p.page_size, p.num_pages, w.step ? 2 : 4,
                                  p.kv_e4m3 ? (p.act_f16 ? 2 : 1) : 0, p.k_scale, p.v_scale,
                                  p.status, st) != cudaSuccess)
       return CPA_ERR_CUDA;
-    const cudaError_t e = single ? launch_window_decode(p, grid, st) : launch_window_f32(p, grid, st);
-    return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    if (!beside) {
+      const cudaError_t e = single ? launch_window_decode(p, grid, st) : launch_window_f32(p, grid, st);
+      return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+    }
+    p.rows_mode = 1;
   }
   if (w.step) {
     // One launch pair for the whole step: the plan (with the append when it
@@ -254,7 +260,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     sw.chunk_o = reinterpret_cast<float *>(ws + w.chunk_o);
     sw.chunk_ml = reinterpret_cast<float2 *>(ws + w.chunk_ml);
     sw.grid = grid;
-    if (nr.k) {
+    if (nr.k && !beside) {
       p.fused = 1;
       p.k_new = nr.k;
       p.v_new = nr.v;
@@ -265,6 +271,10 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     if (p.kv_e4m3) e = win.window ? launch_step<2, true>(p, sw, st) : launch_step<2, false>(p, sw, st);
     else if (p.act_f16) e = win.window ? launch_step<1, true>(p, sw, st) : launch_step<1, false>(p, sw, st);
     else e = win.window ? launch_step<0, true>(p, sw, st) : launch_step<0, false>(p, sw, st);
+    if (e == cudaSuccess && beside) {
+      p.rows_mode = 2;
+      e = launch_window_decode(p, grid, st);
+    }
     return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
   }
   // row kernel: the append (if any) first, on the same stream

@@ -93,7 +93,8 @@ struct AttnParams {
   // Sliding window (0: none): the row at position x sees key j <= x when
   // j < sinks or j > x - window.
   int window, sinks;
-  int rows_mode;              // row kernel: 0 all tokens, 1 only q_len > 1, 2 only q_len == 1
+  int rows_mode;              // row kernel, and windowed steps: 0 all tokens, 1 only q_len > 1,
+                              // 2 only q_len == 1
   // Fused append (cpa_append_attention_forward, step kernel): the step's new
   // k/v rows [num_tokens][Hkv][D] and their cache slots; the plan kernel
   // copies them into the cache before the step kernel reads it.  fused = 0:
@@ -150,8 +151,10 @@ cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t s
 cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
 
 // A windowed step of single tokens with 16-bit queries (attn_window_decode.cu),
-// the new rows already in the cache.
+// the new rows already in the cache; with rows_mode 2 the single tokens of a
+// mixed step, launched behind the step kernel of its chunks.
 bool window_decode_takes(const AttnParams &p, int sms);
+bool window_decode_beside(const AttnParams &p, int sms);
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream);
 
 // A windowed fp32 step (attn_window_f32.cu), the new rows already in the cache.

@@ -313,3 +313,33 @@ def test_f32_finds_its_sequence(cuda_device, seqs):
     lens = [x + int(y) for x, y in zip(q, torch.randint(0, 60, (seqs,), generator=g))]
     b = make_batch(q, lens, 2, 1, 64, "f32", 21, 3, 4, cuda_device)
     check(b, window_call(b, workspace(b)))
+
+
+@pytest.mark.parametrize("mode", ["bf16-e4m3", "f16-e4m3"])
+@pytest.mark.parametrize("append", [False, True])
+def test_many_single_tokens_beside_chunks_8_bit(cuda_device, mode, append):
+    """Enough single tokens for a kernel beside the chunks' one; results as for any other step, and what comes next on the stream
+    sees all of them."""
+    g = torch.Generator().manual_seed(12)
+    seqs = 60
+    q = [1] * seqs
+    q[7], q[30], q[59] = 33, 200, 2
+    lens = [x + int(y) for x, y in zip(q, torch.randint(0, 3000, (seqs,), generator=g))]
+    b = make_batch(q, lens, 16, 8, 128, mode, 1200, 30, 13, cuda_device)
+    ws, out = workspace(b), torch.empty_like(b["q"])
+    for _ in range(3):
+        out.fill_(float("nan"))
+        window_call(b, ws, append=append, out=out)
+        after = out + 0  # an ordinary kernel right behind the call
+        check(b, after, mode)
+    assert status(b, ws) == ops.CPA_OK
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        window_call(b, ws, append=append, out=out)
+        copied = out + 0
+    out.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(copied, after)
