@@ -249,11 +249,11 @@ def test_release_reports(cuda_device):
     assert d.table[2].tolist() == [-1] * 3 and d.refs.tolist() == pool.refs and d.status() == ops.CPA_ERR_DEVICE
 
 
-@pytest.mark.parametrize("pages", [1, 2, 15, 16, 17, 4095, 4096, 4097, 9000, 70_001])
+@pytest.mark.parametrize("pages", [1, 2, 15, 16, 17, 4095, 4096, 4097, 9000, 16_384, 16_385, 70_001, 131_072, 131_073, 200_001])
 @pytest.mark.parametrize("fill", [0.0, 0.3, 0.9, 1.0])
 def test_compact(cuda_device, pages, fill):
     g = torch.Generator().manual_seed(pages)
-    columns = 40
+    columns = 40 if pages < 100_000 else 1000
     rows = -(-pages // columns) + 2
     pool = Pool(rows, columns, pages)
     held = [x for x, y in enumerate(torch.rand(pages, generator=g).tolist()) if y < fill]
@@ -277,6 +277,21 @@ def test_compact(cuda_device, pages, fill):
     d.compact()  # packed already
     assert d.counts.tolist() == [0, m] and d.pairs() == []
     d.same(pool)
+
+
+def test_compact_a_large_table(cuda_device):
+    """A small pool under more entries than the pool's cluster takes with it: rows that share everything."""
+    pool = Pool.random([4000] * 3, 120, 260, 900, 5)
+    d = Device(pool, cuda_device)
+    for p in (pool, d):
+        p.fork([r % 3 for r in range(117)], list(range(3, 120)))
+        p.release([0, 3], 0, 0)
+        p.release([1] + list(range(4, 120, 3)), 0, 0)
+    moves, m = pool.compact()
+    d.compact()
+    assert d.counts.tolist() == [len(moves), m] and d.pairs() == moves and moves
+    d.same(pool)
+    assert d.status() == ops.CPA_OK
 
 
 def test_compact_reports_entries_without_a_page(cuda_device):
