@@ -228,6 +228,11 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
   }
   __syncthreads();
 
+  // A page without earlier tokens of the row is replaced where there is none, or
+  // where another entry holds it too.  (The references stay as they were before
+  // the call until every row is done.)
+  auto replaced = [&](int e) { return e < 0 || (e < a.num_pages && __ldcg(a.refs + e) > 1); };
+
   // A1: what each row needs.  A row of at most four pages is one thread's; a
   // longer one is counted by its whole warp.
   auto slot_of = [&](int page) {  // the page's place in the hash (it is there, or inserted)
@@ -240,6 +245,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
   for (int s0 = 0; s0 < S; s0 += kExtThreads) {
     const int s = s0 + tid;
     int c0 = 0, c1 = 0, need = 0, head = -1;
+    bool partial = false;  // the first page holds earlier tokens
     if (s < S) {
       const int qs = __ldg(a.starts + s), q = __ldg(a.starts + s + 1) - qs;
       int len = __ldg(a.lens + s);
@@ -255,6 +261,8 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
         c1 = (len - 1) / kPageTokens + 1;
         if ((len - q) % kPageTokens) {
           const int e = a.table[(int64_t)s * a.max_pages + c0];
+          partial = true;
+          need = e < 0;
           if (e >= 0 && e < a.num_pages && a.refs[e] > 1) {
             head = e;
             const int h = slot_of(e);
@@ -265,17 +273,20 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
       }
       s_head[s] = head;
     }
+    // pages of the new tokens alone: the row's first, where it writes to a page
+    // that holds earlier tokens, is A2's
+    if (partial) ++c0;
     const bool wide = c1 - c0 > 4;
     if (!wide)
-      for (int c = c0; c < c1; ++c) need += a.table[(int64_t)s * a.max_pages + c] < 0;
+      for (int c = c0; c < c1; ++c) need += replaced(a.table[(int64_t)s * a.max_pages + c]);
     for (unsigned m = __ballot_sync(0xffffffffu, wide); m; m &= m - 1) {
       const int l = __ffs(m) - 1;
       const int row = __shfl_sync(0xffffffffu, s, l), b = __shfl_sync(0xffffffffu, c0, l),
                 e = __shfl_sync(0xffffffffu, c1, l);
       int sum = 0;
-      for (int c = b + lane; c < e; c += 32) sum += a.table[(int64_t)row * a.max_pages + c] < 0;
+      for (int c = b + lane; c < e; c += 32) sum += replaced(a.table[(int64_t)row * a.max_pages + c]);
       sum = __reduce_add_sync(0xffffffffu, sum);
-      if (lane == l) need = sum;
+      if (lane == l) need += sum;
     }
     if (s < S) s_base[s] = need;
   }
@@ -343,6 +354,13 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
     a.counts[1] = fits ? needed : -needed;
     if (!fits) atomicOr(a.status, STATUS_NO_PAGES);
   }
+  // entry *e becomes the r-th free page; what it held is noted in its place
+  auto take = [&](int32_t *e, int r) {
+    const int page = __ldcg(a.free_list + r), old = *e;
+    a.free_list[r] = old;
+    *e = page;
+    a.refs[page] = 1;
+  };
   if (fits) {
     const int nt = nb * kExtThreads;
     for (int s0 = rank * kExtThreads; s0 < S; s0 += nt) {
@@ -357,12 +375,13 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
         r = s_base[s];
         old = s_head[s];
         if (old >= 0) {
-          const int page = __ldcg(a.free_list + r++);
-          a.table[(int64_t)s * a.max_pages + c0] = page;
-          a.refs[page] = 1;
-          atomicSub(a.refs + old, 1);
           a.copy_src[s_copy[s]] = old;
-          a.copy_dst[s_copy[s]] = page;
+          a.copy_dst[s_copy[s]] = __ldcg(a.free_list + r);
+          take(a.table + (int64_t)s * a.max_pages + c0, r++);
+        }
+        if (q > 0 && (len - q) % kPageTokens) {
+          int32_t *e = a.table + (int64_t)s * a.max_pages + c0;
+          if (old < 0 && *e < 0) take(e, r++);
           ++c0;
         }
       }
@@ -370,11 +389,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
       if (!wide)
         for (int c = c0; c < c1; ++c) {
           int32_t *e = a.table + (int64_t)s * a.max_pages + c;
-          if (*e < 0) {
-            const int page = __ldcg(a.free_list + r++);
-            *e = page;
-            a.refs[page] = 1;
-          }
+          if (replaced(*e)) take(e, r++);
         }
       for (unsigned m = __ballot_sync(0xffffffffu, wide); m; m &= m - 1) {
         const int l = __ffs(m) - 1;
@@ -383,19 +398,21 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
         int at2 = __shfl_sync(0xffffffffu, r, l);
         for (int c = b; c < e; c += 32) {
           int32_t *x = a.table + (int64_t)row * a.max_pages + c + lane;
-          const bool empty = c + lane < e && *x < 0;
-          const unsigned who = __ballot_sync(0xffffffffu, empty);
-          if (empty) {
-            const int page = __ldcg(a.free_list + at2 + __popc(who & ((1u << lane) - 1u)));
-            *x = page;
-            a.refs[page] = 1;
-          }
+          const bool mine2 = c + lane < e && replaced(*x);
+          const unsigned who = __ballot_sync(0xffffffffu, mine2);
+          if (mine2) take(x, at2 + __popc(who & ((1u << lane) - 1u)));
           at2 += __popc(who);
         }
       }
     }
   }
   cluster.sync();
+  // ... and the references given up
+  if (fits)
+    for (int i = rank * kExtThreads + tid; i < needed; i += nb * kExtThreads) {
+      const int old = __ldcg(a.free_list + i);
+      if (old >= 0) atomicSub(a.refs + old, 1);
+    }
 
   // D: the new tokens' slots
   for (int64_t t = (int64_t)rank * kExtThreads + tid; t < a.num_tokens; t += (int64_t)nb * kExtThreads) {

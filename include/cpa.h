@@ -290,12 +290,16 @@ int cpa_fork_sequences(const int32_t *parents, const int32_t *children, int32_t 
  * calls: row s takes q_len = query_start_loc[s + 1] - query_start_loc[s] tokens
  * (0: none), and seq_lens[s] counts them already.  In the order of the rows,
  * and of the pages in each:
- *  - where a position of the new tokens has no page, the row takes the lowest
- *    page that was free before the call;
- *  - where the first new token goes to a page that holds earlier tokens and has
- *    other references left, the row gives its reference up, takes the lowest
- *    free page instead, and the pair (old, new) is listed in copy_src,
- *    copy_dst: the last of several rows that all write to a page keeps it;
+ *  - where the new tokens have no page, the row takes the lowest page that was
+ *    free before the call;
+ *  - where the first of them goes to a page that holds earlier tokens and other
+ *    references, the row gives its reference up, takes the lowest free page
+ *    instead, and the pair (old, new) is listed in copy_src, copy_dst.  If all
+ *    of a page's references are rows that write to it so, the last of them
+ *    keeps it;
+ *  - where a page for new tokens alone (the row was set back to a shorter
+ *    length, say) has other references, the row gives its reference up and takes
+ *    the lowest free page; there is nothing to copy;
  *  - slot_mapping[t] is the slot of every new token t, as cpa_kv_append and
  *    the fused attention calls take it.
  * counts (int32 [2], device): the number of pairs listed, and of pages taken.
@@ -330,7 +334,8 @@ int cpa_release_pages(const int32_t *rows, int32_t num_released, int32_t *block_
 
 /* Packs the pool: afterwards its m live pages are pages 0 .. m - 1.  The j-th
  * free page below m takes the place of the j-th live page from m on; page_refs
- * and every entry of block_table follow, and the pairs (old, new) are listed in
+ * and every entry of block_table (all rows that hold pages of the pool) follow,
+ * and the pairs (old, new) are listed in
  * copy_src, copy_dst (int32 [num_pages / 2] each, written up to the count), to
  * be copied in every layer's cache before anything reads or writes it.
  * counts (int32 [2], device): the number of pairs, and m.  An entry whose page

@@ -55,6 +55,8 @@ class Pool:
         free = [x for x, r in enumerate(self.refs) if r == 0]
         keep = [list(r) for r in self.table], list(self.refs)
         pairs, taken = [], 0
+        held = list(self.refs)  # before the call
+        first = [self.table[s][(self.lens[s] - q) // PAGE] if q and (self.lens[s] - q) % PAGE else -1 for s, q in enumerate(q_lens)]
         for s, q in enumerate(q_lens):
             n = self.lens[s]
             if q == 0:
@@ -62,10 +64,16 @@ class Pool:
             for c in range((n - q) // PAGE, (n - 1) // PAGE + 1):
                 x = self.table[s][c]
                 write = x < 0
-                if not write and c * PAGE < n - q and self.refs[x] > 1:
+                if not write and held[x] > 1 and c * PAGE < n - q:
+                    # the last of the rows that write to it so keeps it, if all its references are theirs
+                    last = len(first) - 1 - first[::-1].index(x)
+                    if not (s == last and first.count(x) == held[x]):
+                        write = True
+                        self.refs[x] -= 1
+                        pairs.append((x, free[taken] if taken < len(free) else -1))
+                elif not write and held[x] > 1:
                     write = True
                     self.refs[x] -= 1
-                    pairs.append((x, free[taken] if taken < len(free) else -1))
                 if write:
                     if taken < len(free):
                         self.table[s][c] = free[taken]

@@ -176,6 +176,39 @@ def test_extend_last_writer_keeps_the_shared_page(cuda_device):
     assert taken == 2 and not pairs
 
 
+def test_extend_after_rows_were_set_back(cuda_device):
+    """Rows whose length went back hold pages behind it; where others hold them too, new tokens do not go there."""
+    pool = Pool.random([150, 64, 40, 500], 12, 40, 120, 6)
+    d = Device(pool, cuda_device)
+    for p in (pool, d):
+        p.fork([0, 0, 1, 2, 3, 3], [4, 5, 6, 7, 8, 9])
+    #      set back inside a page, to a page's edge, to nothing, not at all
+    lens = [20, 48, 0, 500, 150, 32, 64, 40, 17, 400, 0, 0]
+    pool.lens = list(lens)
+    for q in ([40, 20, 30, 1, 1, 1, 0, 3, 300, 90, 5, 0], [1] * 12):
+        pool.lens = [n + x for n, x in zip(pool.lens, q)]
+        d.lens.copy_(i32(pool.lens, cuda_device))
+        slots, pairs, taken = pool.extend(q)
+        assert slots is not None
+        assert d.extend(q).tolist() == slots and d.counts.tolist() == [len(pairs), taken] and d.pairs() == pairs
+        d.same(pool)
+        assert len(set(slots)) == len(slots)
+    assert d.status() == ops.CPA_OK
+
+
+def test_extend_a_row_without_its_partly_filled_page(cuda_device):
+    pool = Pool.random([20, 20], 2, 30, 60, 6)
+    for r in range(2):
+        pool.refs[pool.table[r][1]] = 0
+        pool.table[r][1] = -1
+    d = Device(pool, cuda_device)
+    pool.lens = [21, 320]
+    d.lens.copy_(i32(pool.lens, cuda_device))
+    slots, pairs, taken = pool.extend([1, 300])
+    assert d.extend([1, 300]).tolist() == slots and d.counts.tolist() == [0, taken] and not pairs
+    d.same(pool)
+
+
 def test_extend_too_few_pages_changes_nothing(cuda_device):
     pool = Pool.random([16, 20], 4, 5, 6, 2)
     d = Device(pool, cuda_device)
