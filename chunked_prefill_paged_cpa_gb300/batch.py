@@ -24,7 +24,10 @@ def pages_for(num_tokens: int, page_size: int) -> int:
 
 class PageAllocator:
     """Hands out physical pages in a given (normally random) order.  The pool
-    holds ``len(order)`` pages; pages are never freed within a workload."""
+    holds ``len(order)`` pages; pages are never freed within a workload.  (A pool
+    on the device, whose pages are shared and given back, is kept by
+    ``ops.fork_sequences``, ``extend_sequences``, ``release_pages`` and
+    ``compact_pages``.)"""
 
     def __init__(self, order: torch.Tensor):
         self.order = [int(x) for x in order.tolist()]
