@@ -303,6 +303,8 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
     after_o();
   };
 
+  // the append that may have been launched just before
+  if (p.rows_mode != 2) ptx::grid_dependency_wait();
   // The next page is on its way while a page is computed.  16-bit caches: into
   // a second set of registers.  8-bit caches, whose pages are half as long:
   // K's words as soon as S has used K's registers, V's after O has used V's; the
@@ -467,7 +469,7 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.rows_mode == 2 ? 2 : 1;
+  cfg.numAttrs = p.rows_mode == 2 || p.fused ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D>, p);
 }
 

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // rows r and r + 8
   const float sl2 = p.scale_log2;
 
+  ptx::grid_dependency_wait();  // the append that may have been launched just before
   UnitRegs<D> x;
   int64_t at = 0;
   int e = -1;
@@ -369,10 +370,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
+// Q of four tiles; or Q of one tile, later the warps' O and the CTA's.
+template <int D, bool ROWS>
+constexpr int smem_bytes() {
+  return (ROWS ? kWarps * kRows * D * 2 : (kWarps + 1) * kRows * D) * (int)sizeof(float);
+}
+
+// CTAs resident on an SM at a time (one tile per CTA).
+template <int D>
+int resident() {
+  static const int ctas = [] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false>, kWarps * 32,
+                                                      smem_bytes<D, false>()) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return std::max(n, 1);
+  }();
+  return ctas;
+}
+
 template <int D, bool ROWS>
 cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
-  // Q of four tiles; or Q of one tile, later the warps' O and the CTA's
-  const int smem = (ROWS ? kWarps * kRows * D * 2 : (kWarps + 1) * kRows * D) * (int)sizeof(float);
+  constexpr int smem = smem_bytes<D, ROWS>();
   const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D, ROWS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -382,12 +403,14 @@ cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = nc;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.fused ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, ROWS>, p);
 }
 
@@ -398,12 +421,21 @@ cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream)
   const int64_t tiles = (int64_t)p.Hkv * (((int64_t)p.num_tokens * G + kRows - 1) / kRows);
   if (p.num_tokens > p.num_seqs && tiles >= 8 * sms)  // two CTAs of four tiles on every SM
     return p.D == 128 ? launch<128, true>(p, 1, stream) : launch<64, true>(p, 1, stream);
-  // CTAs per tile: enough to give every SM one, as long as every warp has a page
+  // CTAs per tile: the number with the fewest rounds of resident CTAs, counted
+  // in a warp's pages, a start and a join costing about three
   const int64_t pages = std::min<int64_t>(
       p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 2 + (p.sinks + kPageKeys - 1) / kPageKeys);
   const int64_t ctas = std::max<int64_t>(tiles, (int64_t)p.Hkv * p.num_seqs);
+  const int64_t slots = (int64_t)sms * (p.D == 128 ? resident<128>() : resident<64>());
   int nc = 1;
-  while (nc < 8 && ctas * nc <= sms && pages > (int64_t)nc * kWarps) nc *= 2;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= 8; n *= 2) {
+    const int64_t cost = (ctas * n + slots - 1) / slots * ((pages + n * kWarps - 1) / (n * kWarps) + 3);
+    if (cost < least) {
+      least = cost;
+      nc = n;
+    }
+  }
   return p.D == 128 ? launch<128, false>(p, nc, stream) : launch<64, false>(p, nc, stream);
 }
 

@@ -242,6 +242,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
                                  p.status, st) != cudaSuccess)
       return CPA_ERR_CUDA;
     if (!beside) {
+      p.fused = nr.k != nullptr;
       const cudaError_t e = single ? launch_window_decode(p, grid, st) : launch_window_f32(p, grid, st);
       return e == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
     }

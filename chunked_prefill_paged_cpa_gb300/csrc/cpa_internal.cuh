@@ -98,7 +98,9 @@ struct AttnParams {
   // Fused append (cpa_append_attention_forward, step kernel): the step's new
   // k/v rows [num_tokens][Hkv][D] and their cache slots; the plan kernel
   // copies them into the cache before the step kernel reads it.  fused = 0:
-  // the cache already holds them (cpa_kv_append ran first).
+  // the cache already holds them (cpa_kv_append ran first).  The windowed kernels
+  // of fp32 steps and of single tokens: the append is the launch just before,
+  // and they wait for it themselves.
   int fused;
   const void *k_new;
   const void *v_new;

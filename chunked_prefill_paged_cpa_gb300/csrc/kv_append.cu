@@ -25,6 +25,9 @@ kv_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                  void *__restrict__ v_cache, int64_t num_tokens, int Hkv,
                  int chunks_per_row, int page_size, int64_t num_slots,
                  float k_scale, float v_scale, uint32_t *status) {
+  // an attention kernel launched behind this one with programmatic serialisation
+  // may start (it waits for this grid before it reads the cache)
+  ptx::grid_launch_dependents();
   const int64_t total = num_tokens * Hkv * chunks_per_row;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
