@@ -374,6 +374,12 @@ def _expect_any(name: str, t: torch.Tensor, dtype, dims: int, index: int):
     return _expect(name, t, dtype, shape, index), shape
 
 
+def _i32(x) -> int:
+    """A window or a number of sinks as the library takes it: what is larger
+    means the same as the largest, and every negative is refused."""
+    return min(max(int(x), -1), 2 ** 31 - 1)
+
+
 _DTYPES = {torch.float32: CPA_F32, torch.bfloat16: CPA_BF16, torch.float16: CPA_F16}
 
 
@@ -426,7 +432,7 @@ def window_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, 
     out, index, at, to, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc,
                                             seq_lens, workspace, out, k_scale, v_scale)
     _launch("cpa_window_attention_forward", load().cpa_window_attention_forward, index, stream,
-            (*at, scale, window, sinks, to), desc, True)
+            (*at, float(scale), _i32(window), _i32(sinks), to), desc, True)
     return out
 
 
@@ -441,7 +447,7 @@ def append_window_attention_forward(q, k, v, slot_mapping, k_cache, v_cache, blo
     new = (_expect("k", k, q.dtype, rows, index), _expect("v", v, q.dtype, rows, index),
            _expect("slot_mapping", slot_mapping, torch.int64, rows[:1], index))
     _launch("cpa_append_window_attention_forward", load().cpa_append_window_attention_forward, index,
-            stream, (at[0], *new, *at[1:], scale, window, sinks, to), desc, True)
+            stream, (at[0], *new, *at[1:], float(scale), _i32(window), _i32(sinks), to), desc, True)
     return out
 
 
@@ -523,8 +529,8 @@ def release_pages(rows, block_table, seq_lens, page_refs, workspace, window=0, s
     n, which = every, None
     if rows is not None:
         which, (n,) = _expect_any("rows", rows, torch.int32, 1, index)
-    at = (which, n, table, _expect("seq_lens", seq_lens, torch.int32, (every,), index), every, window,
-          sinks, refs)
+    at = (which, n, table, _expect("seq_lens", seq_lens, torch.int32, (every,), index), every,
+          _i32(window), _i32(sinks), refs)
     _launch("cpa_release_pages", load().cpa_release_pages, index, stream, at, desc, False)
 
 

@@ -453,3 +453,56 @@ def test_captured_and_replayed(cuda_device):
         for t, x in zip((d.table, d.lens, d.refs, kc, vc, slots, d.counts), want):
             assert torch.equal(t, x)
     assert q and d.status() == ops.CPA_OK
+
+
+def test_tensors_that_are_refused(cuda_device):
+    pool = Pool.random([30, 30], 4, 6, 40, 3)
+    d = Device(pool, cuda_device)
+    rows = i32([0, 1], cuda_device)
+    with pytest.raises(ValueError):
+        ops.fork_sequences(rows, rows[:1], d.table, d.lens, d.refs, d.ws)
+    with pytest.raises(ValueError):
+        ops.fork_sequences(rows, rows, d.table[:, ::2], d.lens, d.refs, d.ws)
+    with pytest.raises(TypeError):
+        ops.release_pages(rows.long(), d.table, d.lens, d.refs, d.ws)
+    with pytest.raises(ValueError):
+        ops.release_pages(rows, d.table, d.lens[:3], d.refs, d.ws)
+    with pytest.raises(ValueError):  # lists too short
+        ops.compact_pages(d.table, d.refs, d.src[:19], d.dst, d.counts, d.ws)
+    with pytest.raises(ops.CpaError):  # references off a 16-byte boundary
+        ops.compact_pages(d.table, d.refs[1:], d.src, d.dst, d.counts, d.ws)
+    with pytest.raises(ops.CpaError):  # a workspace for fewer pages
+        ops.compact_pages(d.table, d.refs, d.src, d.dst, d.counts, d.ws[:256])
+    with pytest.raises(ops.CpaError):
+        ops.release_pages(rows, d.table, d.lens, d.refs, d.ws, window=-5)
+    with pytest.raises(ops.CpaError):  # sinks without a window
+        ops.release_pages(rows, d.table, d.lens, d.refs, d.ws, sinks=3)
+    d.same(pool)
+    assert d.status() == ops.CPA_OK
+
+
+def test_on_another_stream(cuda_device):
+    """The whole flow on a stream of its own, with the host's stream idle."""
+    pool = Pool.random([100, 37], 4, 12, 40, 4)
+    d = Device(pool, cuda_device)
+    kc = torch.randn(40, 2, PAGE, 64, device=cuda_device)
+    vc, before = kc.clone(), kc.clone()
+    starts, slots = i32(range(5), cuda_device), torch.zeros(4, dtype=torch.int64, device=cuda_device)
+    parents, kids, gone = i32([0, 1], cuda_device), i32([2, 3], cuda_device), i32([0], cuda_device)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ops.fork_sequences(parents, kids, d.table, d.lens, d.refs, d.ws, stream=s)
+    with torch.cuda.stream(s):
+        d.lens.add_(1)
+    ops.extend_sequences(starts, d.lens, d.table, d.refs, slots, d.src, d.dst, d.counts, d.ws, stream=s)
+    ops.copy_pages(d.src, d.dst, kc, vc, num_pairs=d.counts, workspace=d.ws, stream=s)
+    ops.release_pages(gone, d.table, d.lens, d.refs, d.ws, stream=s)
+    s.synchronize()
+    pool.fork([0, 1], [2, 3])
+    pool.lens = [n + 1 for n in pool.lens]
+    want, pairs, _ = pool.extend([1] * 4)
+    pool.release([0])
+    d.same(pool)
+    assert slots.tolist() == want and pairs
+    for a, b in pairs:
+        assert torch.equal(kc[b], before[a]) and torch.equal(vc[b], before[a])

@@ -343,3 +343,81 @@ def test_many_single_tokens_beside_chunks_8_bit(cuda_device, mode, append):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(copied, after)
+
+
+# ---- what the documentation allows and little else reaches
+
+@pytest.mark.parametrize("mode", ["bf16", "f16", "bf16-e4m3"])
+@pytest.mark.parametrize("hq,hkv,window", [(8, 2, 20_000), (4, 1, 2 ** 40)])
+def test_few_tokens_with_a_very_long_window(cuda_device, mode, hq, hkv, window):
+    b = make_batch([1, 1], [30_000, 21_001], hq, hkv, 64, mode, min(window, 2 ** 30), 100, 14, cuda_device)
+    ws = workspace(b)
+    b["window"] = window
+    out = window_call(b, ws, append=True)
+    b["window"] = min(window, 2 ** 30)
+    check(b, out, mode)
+    assert status(b, ws) == ops.CPA_OK
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "bf16-e4m3"])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [1, 40, 1]])
+def test_pages_beyond_32_bit_offsets(cuda_device, mode, q_lens):
+    """The same step with its pages at the end of a cache of more than 2^32 elements: the same bits."""
+    b = make_batch(q_lens, [700, 300, 90], 16, 8, 128, mode, 250, 20, 15, cuda_device)
+    want = window_call(b, workspace(b))
+    n = b["k_cache"].shape[0]
+    first = 2 ** 32 // (8 * 16 * 128) + 5
+    far = dict(b)
+    for c in ("k_cache", "v_cache"):
+        far[c] = torch.empty((first + n, *b[c].shape[1:]), dtype=b[c].dtype, device=cuda_device)
+        far[c][first:] = b[c]
+    far["table"] = torch.where(b["table"] >= 0, b["table"] + first, -1)
+    far["slots"] = b["slots"] + first * 16
+    ws = workspace(far)
+    got = window_call(far, ws, append=True)
+    assert status(far, ws) == ops.CPA_OK
+    assert torch.equal(got, want)
+    src = torch.arange(first, first + n, dtype=torch.int32, device=cuda_device)
+    ops.copy_pages(src, src - first, far["k_cache"], far["v_cache"])
+    assert torch.equal(far["k_cache"][:n].view(torch.uint8), b["k_cache"].view(torch.uint8))
+
+
+def test_rows_behind_the_last_sequence_stay(cuda_device):
+    """Tokens that no sequence owns: their output is left as it was."""
+    for mode in MODES:
+        for q in ([1, 1], [1, 30]):
+            b = make_batch(q, [80, 90], 4, 2, 64, mode, 30, 4, 16, cuda_device)
+            T = sum(q)
+            pad = torch.randn(5, 4, 64, device=cuda_device).to(b["q"].dtype)
+            long = dict(b, q=torch.cat([b["q"], pad]))
+            out = torch.full_like(long["q"], 7)
+            ws = workspace(long)
+            ops.window_attention_forward(long["q"], long["k_cache"], long["v_cache"], long["table"], long["starts"],
+                                         long["lens"], long["scale"], ws, 30, 4, out=out, **long["scales"])
+            check(b, out[:T], mode)
+            assert (out[T:] == 7).all()
+
+
+def test_tensors_that_are_refused(cuda_device):
+    b = make_batch([1, 1], [80, 90], 4, 2, 64, "bf16", 30, 4, 16, cuda_device)
+    ws = workspace(b)
+    good = dict(b)
+
+    def call(**kw):
+        return window_call(dict(good, **kw), kw.pop("ws", ws))
+
+    wide = torch.zeros((2, 2 * b["table"].shape[1]), dtype=torch.int32, device=cuda_device)
+    for kw in (dict(table=wide[:, ::2]), dict(lens=b["lens"][:1]), dict(starts=b["starts"][:2]), dict(v_cache=b["v_cache"][1:]),
+               dict(k_cache=b["k_cache"].transpose(1, 2)), dict(q=b["q"][:, :, :32]), dict(table=b["table"].cpu()),
+               dict(q=b["q"].expand(2, 4, 64)[:, ::2]), dict(ws=ws.view(torch.int32))):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    for kw in (dict(lens=b["lens"].long()), dict(q=b["q"].half())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(window=0), dict(window=-2 ** 40), dict(sinks=-1), dict(ws=ws[256:512]), dict(scale=float("nan"))):
+        with pytest.raises(ops.CpaError):
+            call(**kw)
+    with pytest.raises(ValueError):
+        window_call(good, ws, out=torch.empty_like(b["q"])[:1])
+    check(b, call())
