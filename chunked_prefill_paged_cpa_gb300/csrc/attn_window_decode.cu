@@ -30,7 +30,7 @@ namespace cpa {
 namespace {
 
 constexpr int kPageKeys = 16;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                  // of a CTA that may share its row with a cluster
 constexpr int kMaxCluster = 8;            // (portable)
 constexpr int kHeads = 8;                 // N of the MMAs
 constexpr float kMoveThreshold = 8.0f;    // log2 units, as in the step kernel
@@ -113,8 +113,8 @@ struct PageRegs {
   }
 };
 
-template <int KVM, int D>
-__global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnParams p) {
+template <int KVM, int D, int W>
+__global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams p) {
   constexpr bool F16 = KVM != 0;
   constexpr int EB = KVM == 2 ? 1 : 2;
   constexpr int KS = D / 16;   // k-steps of S, and 16-dim tiles of O^T
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   const int sink_pages = (near + kPageKeys - 1) / kPageKeys;
   const int gap = max(0, far / kPageKeys - sink_pages);
   const int np = (vis + kPageKeys - 1) / kPageKeys - gap;
-  const int wi = rank * kWarps + warp, nw = nc * kWarps;
+  const int wi = rank * W + warp, nw = nc * W;
   const int v0 = (int)((int64_t)np * wi / nw), v1 = (int)((int64_t)np * (wi + 1) / nw);
 
   // Q as the B operand: head r, the dims that K's lanes with this c hold, in
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
   }
 
   // join the warps, then the cluster's CTAs
-  __shared__ float sm_o[kWarps][kHeads][D];
-  __shared__ float2 sm_ml[kWarps][kHeads];
+  __shared__ float sm_o[W][kHeads][D];
+  __shared__ float2 sm_ml[W][kHeads];
 #pragma unroll
   for (int k = 4; k < 32; k <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, k);
@@ -396,22 +396,22 @@ __global__ void __launch_bounds__(kWarps * 32) window_decode_kernel(const AttnPa
         f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
   };
   auto of_warps = [&](int h, int d) {
-    return join(kWarps, [&](int w) { return sm_ml[w][h]; }, [&](int w) { return sm_o[w][h][d]; });
+    return join(W, [&](int w) { return sm_ml[w][h]; }, [&](int w) { return sm_o[w][h][d]; });
   };
   if (nc == 1) {
-    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) store(i / D, i % D, of_warps(i / D, i % D));
+    for (int i = threadIdx.x; i < G * D; i += W * 32) store(i / D, i % D, of_warps(i / D, i % D));
     ptx::grid_dependency_wait();
     return;
   }
   __shared__ float cl_o[kHeads][D];
   __shared__ float2 cl_ml[kHeads];
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < G * D; i += W * 32) {
     const State x = of_warps(i / D, i % D);
     cl_o[i / D][i % D] = x.O;
     if (i % D == 0) cl_ml[i / D] = make_float2(x.M, x.L);
   }
   cluster.sync();
-  for (int i = rank * kWarps * 32 + threadIdx.x; i < G * D; i += nc * kWarps * 32) {
+  for (int i = rank * W * 32 + threadIdx.x; i < G * D; i += nc * W * 32) {
     const int h = i / D, d = i % D;
     store(h, d, join(nc, [&](int b) { return *cluster.map_shared_rank(&cl_ml[h], b); },
                      [&](int b) { return *cluster.map_shared_rank(&cl_o[h][d], b); }));
@@ -428,39 +428,31 @@ int64_t page_bound(const AttnParams &p) {
                                             (p.sinks + kPageKeys - 1) / kPageKeys);
 }
 
-template <int KVM, int D>
-cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
-  // CTAs per (token, kv head): the number with the fewest rounds of resident
-  // CTAs, counted in a warp's pages, a start and a join costing about three
-  static const int resident = [] {
+template <int KVM, int D, int W>
+int resident() {  // CTAs on an SM at a time
+  static const int ctas = [] {
     int n = 0;
     // The words on their way sit in L1: an SM that the step kernel has left comes
     // with nearly all of it as shared memory, and is to be set up anew.  (64
     // tokens of window 4096 beside a 480-token chunk, 8-bit cache: 192 us without
     // this hint, 151 us with it.)
-    if (cudaFuncSetAttribute(window_decode_kernel<KVM, D>,
-                             cudaFuncAttributePreferredSharedMemoryCarveout, 40) != cudaSuccess)
-      cudaGetLastError();
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D>, kWarps * 32, 0) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(window_decode_kernel<KVM, D, W>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout, 40) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D, W>, W * 32, 0) !=
+            cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
     return std::max(n, 1);
   }();
-  const int64_t rows = (int64_t)(p.rows_mode == 2 ? p.num_seqs : p.num_tokens) * p.Hkv, slots = (int64_t)resident * sms, pages = page_bound(p);
-  int nc = 1;
-  int64_t least = INT64_MAX;
-  for (int n = 1; n <= kMaxCluster; n *= 2) {
-    const int64_t cost = (rows * n + slots - 1) / slots * ((pages + n * kWarps - 1) / (n * kWarps) + 3);
-    if (cost < least) {
-      least = cost;
-      nc = n;
-    }
-  }
+  return ctas;
+}
+
+template <int KVM, int D, int W>
+cudaError_t launch_on(const AttnParams &p, int nc, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc, p.Hkv, p.rows_mode == 2 ? p.num_seqs : p.num_tokens);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(W * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -470,7 +462,35 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.rows_mode == 2 || p.fused ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D>, p);
+  return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D, W>, p);
+}
+
+template <int KVM, int D>
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
+  // CTAs per (token, kv head): the number with the fewest rounds of resident
+  // CTAs, counted in a warp's pages, a start and a join costing about three
+  const int64_t rows = (int64_t)(p.rows_mode == 2 ? p.num_seqs : p.num_tokens) * p.Hkv;
+  const int64_t slots = (int64_t)resident<KVM, D, kWarps>() * sms, pages = page_bound(p);
+  if constexpr (KVM == 2) {
+    // Rows for more than one round, over an 8-bit cache: CTAs of two warps, since
+    // starts and joins weigh more beside the shorter pages (256 tokens of 8 kv
+    // heads: window 1024 97 / 90 us, 4096 339 / 320 us with four and with two warps;
+    // 64 tokens, one round, 85 / 89 us).
+    if (rows > slots) {
+      resident<KVM, D, 2>();
+      return launch_on<KVM, D, 2>(p, 1, stream);
+    }
+  }
+  int nc = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= kMaxCluster; n *= 2) {
+    const int64_t cost = (rows * n + slots - 1) / slots * ((pages + n * kWarps - 1) / (n * kWarps) + 3);
+    if (cost < least) {
+      least = cost;
+      nc = n;
+    }
+  }
+  return launch_on<KVM, D, kWarps>(p, nc, stream);
 }
 
 }  // namespace

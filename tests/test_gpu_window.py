@@ -421,3 +421,15 @@ def test_tensors_that_are_refused(cuda_device):
     with pytest.raises(ValueError):
         window_call(good, ws, out=torch.empty_like(b["q"])[:1])
     check(b, call())
+
+
+@pytest.mark.parametrize("mode", ["bf16-e4m3", "f16-e4m3", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_tokens_of_many_rows(cuda_device, mode, d):
+    """More rows than the SMs hold at a time."""
+    g = torch.Generator().manual_seed(17)
+    lens = torch.randint(1, 300, (1500,), generator=g).tolist()
+    b = make_batch([1] * 1500, lens, 8, 4, d, mode, 130, 9, 18, cuda_device)
+    ws = workspace(b)
+    check(b, window_call(b, ws), mode)
+    assert status(b, ws) == ops.CPA_OK
