@@ -27,6 +27,37 @@ constexpr int kPageTokens = 16;
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
+// These calls come one after another on a stream, each waiting for the one
+// before, and most are shorter than a launch: they are launched with
+// programmatic serialisation, let the next one in at once, and wait for the one
+// before (its writes visible) before they read or write anything.  A copy, which
+// fills the SMs, lets the next one in when it ends.  (Release,
+// release, compact and copy on 96 rows 98.7 -> 95.4 us, on 6 rows 15.2 -> 12.1 us.)
+__device__ __forceinline__ void chain() {
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+}
+
+// kernel<<<grid, threads, smem, stream>>>(args...), in clusters along x, so.
+template <class... Params, class... Args>
+int launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                   int cluster, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------------------
 // Copies.  The 16-byte words of all pairs' K and V pages are numbered through
 // (pair, then K or V, then the word within the page); a block takes 1024
@@ -38,6 +69,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
                   const int32_t *__restrict__ num_pairs, int max_pairs, uint4 *k_cache,
                   uint4 *v_cache, int page_words, int64_t num_pages, uint32_t *status) {
+  ptx::grid_dependency_wait();
   int n = max_pairs;
   if (num_pairs) n = min(max(__ldg(num_pairs), 0), max_pairs);
   const int pair_words = 2 * page_words;
@@ -82,6 +114,7 @@ __global__ void __launch_bounds__(kRowThreads)
 fork_kernel(const int32_t *__restrict__ parents, const int32_t *__restrict__ children, int n,
             int32_t *table, int max_pages, int32_t *seq_lens, int num_rows, int32_t *refs,
             int64_t num_pages, uint32_t *status) {
+  chain();
   const int i = blockIdx.x, tid = threadIdx.x;
   const int parent = __ldg(parents + i), child = __ldg(children + i);
   int bad = parent < 0 || parent >= num_rows || child < 0 || child >= num_rows;
@@ -120,6 +153,7 @@ __global__ void __launch_bounds__(kRowThreads)
 release_kernel(const int32_t *__restrict__ rows, int32_t *table, int max_pages, int32_t *seq_lens,
                int num_rows, int window, int sinks, int32_t *refs, int64_t num_pages,
                uint32_t *status) {
+  chain();
   const int row = rows ? __ldg(rows + blockIdx.x) : (int)blockIdx.x;
   if (row < 0 || row >= num_rows) {
     if (threadIdx.x == 0) atomicOr(status, STATUS_BAD_ROW);
@@ -203,6 +237,7 @@ inline size_t extend_smem(int num_seqs, int hash_bits) {
 }
 
 __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a) {
+  chain();
   cg::cluster_group cluster = cg::this_cluster();
   const int nb = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
@@ -465,6 +500,7 @@ __device__ __forceinline__ unsigned live_bits(const int32_t *refs, int64_t p, in
 
 __global__ void __launch_bounds__(kCompactThreads)
 compact_count_kernel(const int32_t *refs, int64_t num_pages, int32_t *block_live) {
+  chain();
   __shared__ int64_t warps[32];
   const int64_t p = (int64_t)blockIdx.x * kCompactBlock + threadIdx.x * kCompactPages;
   int64_t total;
@@ -499,6 +535,7 @@ __device__ __forceinline__ void list_pages(int64_t p, unsigned live, int64_t num
 __global__ void __launch_bounds__(kCompactThreads)
 compact_place_kernel(const int32_t *refs, int64_t num_pages, const int32_t *block_live,
                      int32_t *copy_src, int32_t *copy_dst, int32_t *counts, int32_t *place) {
+  chain();
   __shared__ int64_t warps[32];
   const int tid = threadIdx.x, nblocks = gridDim.x;
   // live pages in all, and before this block
@@ -558,6 +595,7 @@ __global__ void __launch_bounds__(256)
 compact_apply_kernel(int32_t *table, int64_t entries, int32_t *refs, int64_t num_pages,
                      const int32_t *copy_src, const int32_t *copy_dst, const int32_t *counts,
                      const int32_t *place, uint32_t *status) {
+  chain();
   compact_apply(table, entries, refs, num_pages, copy_src, copy_dst, counts[0], counts[1], place, status,
                 (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
 }
@@ -567,6 +605,7 @@ __global__ void __launch_bounds__(kExtThreads)
 compact_cluster_kernel(int32_t *refs, int64_t num_pages, int32_t *copy_src, int32_t *copy_dst,
                        int32_t *counts, int32_t *place, int32_t *table, int64_t entries, int apply,
                        uint32_t *status) {
+  chain();
   cg::cluster_group cluster = cg::this_cluster();
   const int nb = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
   __shared__ int64_t warps[32];
@@ -623,8 +662,6 @@ int check_pool(const cpa_desc *d, const void *table, int rows, const void *refs)
   return CPA_OK;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? CPA_OK : CPA_ERR_CUDA; }
-
 }  // namespace
 }  // namespace cpa
 
@@ -658,10 +695,9 @@ extern "C" int cpa_copy_pages(const int32_t *src, const int32_t *dst, const int3
   if (sms <= 0) return CPA_ERR_CUDA;
   const int64_t step = kCopyThreads * kCopyWords;
   const int64_t blocks = ((int64_t)max_pairs * 2 * words + step - 1) / step;
-  copy_pages_kernel<<<(int)std::min<int64_t>(blocks, 16 * sms), kCopyThreads, 0, (cudaStream_t)stream>>>(
-      src, dst, num_pairs, max_pairs, static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache),
+  return launch_chained(
+      copy_pages_kernel, dim3((unsigned)std::min<int64_t>(blocks, 16 * sms)), kCopyThreads, 0, (cudaStream_t)stream, 0, src, dst, num_pairs, max_pairs, static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache),
       (int)words, desc->num_pages, status);
-  return launched();
 }
 
 extern "C" int cpa_fork_sequences(const int32_t *parents, const int32_t *children,
@@ -676,10 +712,9 @@ extern "C" int cpa_fork_sequences(const int32_t *parents, const int32_t *childre
   if (!parents || !children || !seq_lens || !aligned(parents, 4) || !aligned(children, 4) ||
       !aligned(seq_lens, 4))
     return CPA_ERR_ARG;
-  fork_kernel<<<num_forks, kRowThreads, 0, (cudaStream_t)stream>>>(
-      parents, children, num_forks, block_table, desc->max_pages_per_seq, seq_lens, num_rows,
+  return launch_chained(
+      fork_kernel, dim3(num_forks), kRowThreads, 0, (cudaStream_t)stream, 0, parents, children, num_forks, block_table, desc->max_pages_per_seq, seq_lens, num_rows,
       page_refs, desc->num_pages, static_cast<uint32_t *>(desc->workspace));
-  return launched();
 }
 
 extern "C" int cpa_release_pages(const int32_t *rows, int32_t num_released, int32_t *block_table,
@@ -695,11 +730,10 @@ extern "C" int cpa_release_pages(const int32_t *rows, int32_t num_released, int3
   if (!seq_lens || !aligned(rows, 4) || !aligned(seq_lens, 4)) return CPA_ERR_ARG;
   const int64_t runs = ((int64_t)desc->max_pages_per_seq + kReleaseCols - 1) / kReleaseCols;
   if (runs > 65535) return CPA_ERR_UNSUPPORTED;
-  release_kernel<<<dim3(num_released, (unsigned)runs), kRowThreads, 0, (cudaStream_t)stream>>>(
-      rows, block_table, desc->max_pages_per_seq, seq_lens, num_rows, std::min(window, 1 << 30),
+  return launch_chained(
+      release_kernel, dim3(num_released, (unsigned)runs), kRowThreads, 0, (cudaStream_t)stream, 0, rows, block_table, desc->max_pages_per_seq, seq_lens, num_rows, std::min(window, 1 << 30),
       std::min(sinks, 1 << 30), page_refs, desc->num_pages,
       static_cast<uint32_t *>(desc->workspace));
-  return launched();
 }
 
 extern "C" int cpa_extend_sequences(const int32_t *query_start_loc, const int32_t *seq_lens,
@@ -740,18 +774,7 @@ extern "C" int cpa_extend_sequences(const int32_t *query_start_loc, const int32_
   // 4 K tokens, at most eight, the largest portable cluster.
   const int64_t want = std::max((desc->num_pages + 16383) / 16384, (desc->num_tokens + 4095) / 4096);
   const int nb = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nb);
-  cfg.blockDim = dim3(kExtThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = nb;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, extend_kernel, a) == cudaSuccess ? CPA_OK : CPA_ERR_CUDA;
+  return launch_chained(extend_kernel, dim3(nb), kExtThreads, smem, (cudaStream_t)stream, nb, a);
 }
 
 extern "C" int cpa_compact_pages(int32_t *block_table, int32_t num_rows, int32_t *page_refs,
@@ -775,28 +798,18 @@ extern "C" int cpa_compact_pages(int32_t *block_table, int32_t num_rows, int32_t
     // the tables here too, up to four entries per thread (a round of dependent
     // loads each; a launch of its own is as quick from there on)
     const int apply = entries <= (int64_t)nb * kExtThreads * 4;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nb);
-    cfg.blockDim = dim3(kExtThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = nb;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, few ? compact_cluster_kernel<kFew> : compact_cluster_kernel<kCompactPages>, page_refs, desc->num_pages, copy_src, copy_dst,
-                           counts, place, block_table, entries, apply, status) != cudaSuccess)
-      return CPA_ERR_CUDA;
+    const int e = launch_chained(few ? compact_cluster_kernel<kFew> : compact_cluster_kernel<kCompactPages>,
+                                 dim3(nb), kExtThreads, 0, st, nb, page_refs, desc->num_pages, copy_src,
+                                 copy_dst, counts, place, block_table, entries, apply, status);
+    if (e != CPA_OK) return e;
     if (apply) return CPA_OK;
   } else {
     const int blocks = (int)((desc->num_pages + kCompactBlock - 1) / kCompactBlock);
-    compact_count_kernel<<<blocks, kCompactThreads, 0, st>>>(page_refs, desc->num_pages, block_live);
-    int e = launched();
+    int e = launch_chained(compact_count_kernel, dim3(blocks), kCompactThreads, 0, st, 0, page_refs,
+                           desc->num_pages, block_live);
     if (e != CPA_OK) return e;
-    compact_place_kernel<<<blocks, kCompactThreads, 0, st>>>(page_refs, desc->num_pages, block_live,
-                                                            copy_src, copy_dst, counts, place);
-    e = launched();
+    e = launch_chained(compact_place_kernel, dim3(blocks), kCompactThreads, 0, st, 0, page_refs,
+                       desc->num_pages, block_live, copy_src, copy_dst, counts, place);
     if (e != CPA_OK) return e;
   }
   int dev = 0;
@@ -804,7 +817,7 @@ extern "C" int cpa_compact_pages(int32_t *block_table, int32_t num_rows, int32_t
   const int sms = sm_count(dev);
   if (sms <= 0) return CPA_ERR_CUDA;
   const int64_t work = std::max(entries, desc->num_pages);
-  compact_apply_kernel<<<(int)std::min<int64_t>((work + 255) / 256, 8 * sms), 256, 0, st>>>(
-      block_table, entries, page_refs, desc->num_pages, copy_src, copy_dst, counts, place, status);
-  return launched();
+  return launch_chained(compact_apply_kernel, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 8 * sms)), 256,
+                        0, st, 0, block_table, entries, page_refs, desc->num_pages, copy_src, copy_dst,
+                        counts, place, status);
 }
