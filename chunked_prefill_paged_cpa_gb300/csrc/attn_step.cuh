@@ -1069,6 +1069,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
               unlock();
               ptx::mma_commit(&bs->s_full[ti]);
               ptx::mma_commit(&bs->k_empty[kvm % C::KST]);
+              if (WIN && n_mine == 1) ptx::mma_commit(&bs->q_empty[qb]);
             }
           }
           for (int j = 0; ok && j < n_mine; ++j) {
@@ -1097,6 +1098,9 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
             if (more) {
               ptx::mma_commit(&bs->s_full[ti]);
               ptx::mma_commit(&bs->k_empty[(kv + 1) % C::KST]);
+              // the tile's last Q K^T: the next item's queries may load while the
+              // last tile's softmax, its P V and the epilogue still run
+              if (WIN && j + 2 == n_mine) ptx::mma_commit(&bs->q_empty[qb]);
             } else {
               ptx::mma_commit(&bs->o_final[ti]);
             }
@@ -1226,7 +1230,9 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           if (ok) ok = observe_through(2 * nt - 1);
         }
         if (ok) {
-          if (n_mine > 0) {
+          if (WIN && !dec && n_mine > 0) {
+            // (committed behind the last Q K^T)
+          } else if (n_mine > 0) {
             ptx::mma_commit(&bs->q_empty[qb]);
           } else {
             ptx::mbar_arrive(&bs->q_empty[qb]);
