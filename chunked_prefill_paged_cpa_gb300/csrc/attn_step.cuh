@@ -1099,7 +1099,8 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
               ptx::mma_commit(&bs->s_full[ti]);
               ptx::mma_commit(&bs->k_empty[(kv + 1) % C::KST]);
               // the tile's last Q K^T: the next item's queries may load while the
-              // last tile's softmax, its P V and the epilogue still run
+              // last tile's softmax, its P V and the epilogue still run (prefill of
+              // 8192 tokens, window 2048: 250 -> 239 us)
               if (WIN && j + 2 == n_mine) ptx::mma_commit(&bs->q_empty[qb]);
             } else {
               ptx::mma_commit(&bs->o_final[ti]);
