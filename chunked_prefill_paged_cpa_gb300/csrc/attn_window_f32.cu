@@ -64,10 +64,12 @@ struct UnitRegs {
   float k[D / 4];
   float v[2][D / 8];
 
+  // (not the read-only path: the append launched just before may still write the
+  // cache when this kernel starts)
   __device__ __forceinline__ void load_k(const float *kp, int r, int c) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(kp + r * D + i * 16 + c * 4));
+      const float4 x = *reinterpret_cast<const float4 *>(kp + r * D + i * 16 + c * 4);
       k[4 * i] = x.x;
       k[4 * i + 1] = x.y;
       k[4 * i + 2] = x.z;
@@ -79,7 +81,7 @@ struct UnitRegs {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(vp + (2 * c + j) * D + i * 32 + r * 4));
+        const float4 x = *reinterpret_cast<const float4 *>(vp + (2 * c + j) * D + i * 32 + r * 4);
         v[j][4 * i] = x.x;
         v[j][4 * i + 1] = x.y;
         v[j][4 * i + 2] = x.z;

@@ -30,12 +30,19 @@ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 // These calls come one after another on a stream, each waiting for the one
 // before, and most are shorter than a launch: they are launched with
 // programmatic serialisation, let the next one in at once, and wait for the one
-// before (its writes visible) before they read or write anything.  A copy, which
+// before (its writes visible) before they read or write anything.  What they
+// read, another may be writing until then: no load takes the read-only path.  A copy, which
 // fills the SMs, lets the next one in when it ends.  (Release,
 // release, compact and copy on 96 rows 98.7 -> 95.4 us, on 6 rows 15.2 -> 12.1 us.)
 __device__ __forceinline__ void chain() {
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
+}
+
+__device__ __forceinline__ int ld32(const int32_t *p) {
+  int x;
+  asm volatile("ld.global.ca.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
 }
 
 // kernel<<<grid, threads, smem, stream>>>(args...), in clusters along x, so.
@@ -71,7 +78,7 @@ copy_pages_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ d
                   uint4 *v_cache, int page_words, int64_t num_pages, uint32_t *status) {
   ptx::grid_dependency_wait();
   int n = max_pairs;
-  if (num_pairs) n = min(max(__ldg(num_pairs), 0), max_pairs);
+  if (num_pairs) n = min(max(ld32(num_pairs), 0), max_pairs);
   const int pair_words = 2 * page_words;
   const int64_t total = (int64_t)n * pair_words;
   constexpr int kStep = kCopyThreads * kCopyWords;
@@ -87,7 +94,7 @@ copy_pages_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ d
       int word = in % pair_words;
       to[i] = nullptr;
       if (pair >= n) continue;
-      const int a = __ldg(src + pair), b = __ldg(dst + pair);
+      const int a = ld32(src + pair), b = ld32(dst + pair);
       if (a < 0 || a >= num_pages || b < 0 || b >= num_pages) {
         if (word == 0 && status) atomicOr(status, STATUS_BAD_PAGE);
         continue;
@@ -116,13 +123,13 @@ fork_kernel(const int32_t *__restrict__ parents, const int32_t *__restrict__ chi
             int64_t num_pages, uint32_t *status) {
   chain();
   const int i = blockIdx.x, tid = threadIdx.x;
-  const int parent = __ldg(parents + i), child = __ldg(children + i);
+  const int parent = ld32(parents + i), child = ld32(children + i);
   int bad = parent < 0 || parent >= num_rows || child < 0 || child >= num_rows;
   if (!bad) {
     // the child is no other fork's child and nobody's parent, and holds nothing:
     // its row is then this block's alone
     for (int j = tid; j < n; j += kRowThreads)
-      bad |= (j != i && __ldg(children + j) == child) || __ldg(parents + j) == child;
+      bad |= (j != i && ld32(children + j) == child) || ld32(parents + j) == child;
     const int32_t *row = table + (int64_t)child * max_pages;
     for (int c = tid; c < max_pages; c += kRowThreads) bad |= row[c] >= 0;
   }
@@ -154,7 +161,7 @@ release_kernel(const int32_t *__restrict__ rows, int32_t *table, int max_pages, 
                int num_rows, int window, int sinks, int32_t *refs, int64_t num_pages,
                uint32_t *status) {
   chain();
-  const int row = rows ? __ldg(rows + blockIdx.x) : (int)blockIdx.x;
+  const int row = rows ? ld32(rows + blockIdx.x) : (int)blockIdx.x;
   if (row < 0 || row >= num_rows) {
     if (threadIdx.x == 0) atomicOr(status, STATUS_BAD_ROW);
     return;
@@ -282,8 +289,8 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
     int c0 = 0, c1 = 0, need = 0, head = -1;
     bool partial = false;  // the first page holds earlier tokens
     if (s < S) {
-      const int qs = __ldg(a.starts + s), q = __ldg(a.starts + s + 1) - qs;
-      int len = __ldg(a.lens + s);
+      const int qs = ld32(a.starts + s), q = ld32(a.starts + s + 1) - qs;
+      int len = ld32(a.lens + s);
       const bool ok = qs >= 0 && q >= 0 && qs + (int64_t)q <= a.num_tokens && len >= q &&
                       len <= (int64_t)a.max_pages * kPageTokens;
       if (!ok && rank == 0) atomicOr(a.status, STATUS_BAD_ROW);
