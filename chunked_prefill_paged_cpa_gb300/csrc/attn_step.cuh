@@ -556,8 +556,9 @@ __device__ __forceinline__ uint16_t cvt_out(float a, bool f16) {
 // One page of E4M3 codes (16 rows x D bytes at `src`, row-major) widened to
 // binary16 in the 128-byte-swizzled layout the MMAs read: row rr of panel p at
 // dst + p * pstride + rr * 128, its 16-byte chunk c at position c ^ (rr & 7).
-// Rows >= zrow (cache slots past the sequence) become zeros, and with a window
-// rows z0 .. z1 - 1 (keys that no row of the item sees).  The codes lie
+// Rows >= zrow (cache slots past the sequence, with a window those past the
+// item's last row) become zeros, and with a window rows z0 .. z1 - 1 (keys that
+// no row of the item sees).  The codes lie
 // inside the page's own destination (the last panel's rows at D = 128, the
 // second half of the rows at D = 64): taken a group of rows at a time, in
 // order, a group's stores land only on its own codes (read before the
@@ -600,6 +601,14 @@ __device__ __forceinline__ void fill_of(int f, int n, bool &is_v, int &t) {
   else if (f == 2 * n - 1) { is_v = true; t = n - 1; }
   else if (f & 1) { is_v = false; t = (f + 1) >> 1; }
   else { is_v = true; t = (f - 2) >> 1; }
+}
+
+// Keys from here on no row of the item sees: the cache slots past the sequence
+// (of `ctx` positions) and, with a window, the tokens of a chunk behind the last
+// row of tile pair mp.
+template <int G, bool WIN>
+__device__ __forceinline__ int item_end(int ctx, int q_len, int mp) {
+  return WIN ? min(ctx, ctx - q_len + 2 * (mp + 1) * (BM / G)) : ctx;
 }
 
 // Derive an item's geometry from its queue entry (every lane computes the same).
@@ -646,6 +655,10 @@ __device__ __forceinline__ int derive_item(const AttnParams &p, const ItemDesc &
     it.n_mine[0] = max(0, min(j1, it.n_kv[0]) - j0);
     it.n_mine[1] = max(0, min(j1, it.n_kv[1]) - j0);
     it.page0 = 0;
+    // (pages past the last are not read: their keys and values are zeros.  8192
+    // tokens, window 2048: 240.9 us; with those pages read, and their V rows zeroed
+    // by the softmax warps, 248.2 us; neither, which lets NaN through, 240.0 us)
+    it.n_pages = ceil_div(item_end<G, WIN>(ctx, d.q_len, it.mp), kPage);
     it.page_end = it.n_pages;
     it.nsplit = nu;
     it.slot = d.b;
@@ -1284,6 +1297,8 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       // row sees them; their V rows are zeroed, since 0 * NaN is NaN inside PV.
       const int z0 = WIN ? p.sinks : 0;
       const int z1 = WIN ? (it.kind == KIND_CHUNK ? ctx - it.q_len + 2 * it.mp * TM : ctx - 1) - p.window + 1 : 0;
+      // The same holds from `end` on, in the page that holds it.
+      const int end = WIN && it.kind == KIND_CHUNK ? item_end<G, WIN>(ctx, it.q_len, it.mp) : ctx;
       vr.begin(it.kind);
       // E4M3 cache: widen the item's fills, in the producer's order, up to
       // fill `last` (this warp: page `warp` of each tile).  Every softmax warp
@@ -1315,10 +1330,10 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           const int key0 = (it.page0 + 8 * (it.j0 + t) + warp) * kPage;  // this page's first key
           if (is_v)
             widen_page<D, WIN>(stage + warp * C::PAGE_BYTES + C::V8_OFF, stage + warp * C::PAGE_BYTES,
-                               kPage * 128, ctx - key0, z0 - key0, z1 - key0, lane);
+                               kPage * 128, end - key0, z0 - key0, z1 - key0, lane);
           else
             widen_page<D, WIN>(stage + warp * kPage * 128 + C::K8_OFF, stage + warp * kPage * 128,
-                               BN * 128, ctx - key0, z0 - key0, z1 - key0, lane);
+                               BN * 128, end - key0, z0 - key0, z1 - key0, lane);
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(conv);
         }
@@ -1400,16 +1415,17 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
             ptx::unpack2(r2, rs0, rs1);
             l_run += rs0 + rs1;
           }
-          // Cache slots at or past ctx in the last page may hold anything (NaN
-          // included) and 0 * NaN is NaN inside PV: zero those V rows first
-          // (an E4M3 cache: already zeroed by the widening).
-          if (KVM != 2 && (key0 + BN > ctx || (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
+          // Cache slots at or past `end` may hold anything (NaN included) and
+          // 0 * NaN is NaN inside PV: zero those V rows first (an E4M3 cache:
+          // already zeroed by the widening).
+          if (KVM != 2 && ((key0 + BN > end && (!WIN || end % kPage)) ||
+                           (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
             const int vst = vr.stage(j);
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bs->v_full[vst], vr.use(j) & 1))) {
               ok = false;
               break;
             }
-            if ((r >= ctx - key0 && r < it.n_pages * kPage - key0) ||
+            if ((r >= end - key0 && r < it.n_pages * kPage - key0) ||
                 (WIN && r >= z0 - key0 && r < z1 - key0)) {
               unsigned char *vrow = v_stage(vst) + (r / kPage) * C::PAGE_BYTES + (r % kPage) * 128;
 #pragma unroll
