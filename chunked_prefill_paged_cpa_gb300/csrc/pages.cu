@@ -522,23 +522,35 @@ __device__ __forceinline__ void list_pages(int64_t p, unsigned live, int64_t num
                                            int64_t packed, int64_t before_p, int32_t *copy_src,
                                            int32_t *copy_dst, int32_t *place) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (p + i >= num_pages) break;
-    const bool l = live >> i & 1u;
-    const int64_t page = p + i;
-    if (page < m) {
-      if (!l) copy_dst[page - before_p] = (int)page;
-    } else {
-      const int j = (int)(before_p - packed);
-      if (l) copy_src[j] = (int)page;
-      place[page] = l ? j : -1;
+  for (int g = 0; g < N; g += 4) {
+    int at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool l = live >> (g + i) & 1u;
+      const int64_t page = p + g + i;
+      at[i] = l ? 0 : -1;
+      if (page < num_pages) {
+        if (page >= m) {
+          if (l) copy_src[at[i] = (int)(before_p - packed)] = (int)page;
+        } else if (!l) {
+          copy_dst[page - before_p] = (int)page;
+        }
+      }
+      before_p += l;
     }
-    before_p += l;
+    if (p + g + 4 <= num_pages) {
+      *reinterpret_cast<int4 *>(place + p + g) = make_int4(at[0], at[1], at[2], at[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p + g + i < num_pages) place[p + g + i] = at[i];
+    }
   }
 }
 
 // Lists: the j-th free page below m (all live pages) takes the j-th live page
-// from m on.  place[page]: for a live page from m on its j, for others there -1.
+// from m on.  place[page]: -1 for a free page, else the j of a live page from m
+// on, and 0 for a live page that stays.
 __global__ void __launch_bounds__(kCompactThreads)
 compact_place_kernel(const int32_t *refs, int64_t num_pages, const int32_t *block_live,
                      int32_t *copy_src, int32_t *copy_dst, int32_t *counts, int32_t *place) {
@@ -591,10 +603,11 @@ __device__ __forceinline__ void compact_apply(int32_t *table, int64_t entries, i
   }
   for (int64_t i = first; i < entries; i += stride) {
     const int page = table[i];
-    if (page < m) continue;
+    if (page < 0) continue;
+    // (not from the references, which change meanwhile)
     const int j = page < num_pages ? __ldcg(place + page) : -1;
-    if (j >= 0) table[i] = __ldcg(copy_dst + j);
-    else atomicOr(status, STATUS_BAD_PAGE);  // an entry whose page counts as free, or is none
+    if (j < 0) atomicOr(status, STATUS_BAD_PAGE);  // an entry whose page counts as free, or is none
+    else if (page >= m) table[i] = __ldcg(copy_dst + j);
   }
 }
 
