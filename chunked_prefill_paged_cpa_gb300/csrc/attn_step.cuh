@@ -1855,26 +1855,29 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
         return cudaErrorInvalidValue;
     }
   }
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G, WIN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  // shared memory beyond the default is granted to a kernel per device
+  const int device = current_device();
+  cudaError_t e = cudaSuccess;
+  static PerDevice configured;
+  if (configured.get(device, [&] {
+        e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G, WIN>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return e == cudaSuccess ? 1 : 0;
+      }) < 1)
+    return e;
   // the plan (with its side work: the fused append, the queries' copy) ...
   const int64_t side = plan_append_pieces<KVM>(p) + plan_q_pieces<KVM>(p);
   const int side_ctas = (int)std::min<int64_t>(w.grid, (side + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
-  static bool plan_configured = false;
-  if (!plan_configured) {
-    cudaError_t e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G, WIN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)plan_smem_bytes(kDecodeMaxSeqs));
-    if (e != cudaSuccess) return e;
-    plan_configured = true;
-  }
+  static PerDevice plan_configured;
+  if (plan_configured.get(device, [&] {
+        e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G, WIN>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)plan_smem_bytes(kDecodeMaxSeqs));
+        return e == cudaSuccess ? 1 : 0;
+      }) < 1)
+    return e;
   attn_plan_kernel<KVM, G, WIN><<<1 + side_ctas, kPlanThreads, plan_smem_bytes(p.num_seqs), stream>>>(p, w);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // ... then the step, allowed to start while the plan finishes
   cudaLaunchConfig_t cfg = {};

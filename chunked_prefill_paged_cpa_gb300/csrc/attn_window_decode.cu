@@ -431,8 +431,9 @@ int64_t page_bound(const AttnParams &p) {
 }
 
 template <int KVM, int D, int W>
-int resident() {  // CTAs on an SM at a time
-  static const int ctas = [] {
+int resident() {  // CTAs on an SM of the current device at a time
+  static PerDevice ctas;
+  return std::max(1, ctas.get(current_device(), [] {
     int n = 0;
     // The words on their way sit in L1: an SM that the step kernel has left comes
     // with nearly all of it as shared memory, and is to be set up anew.  (64
@@ -445,9 +446,8 @@ int resident() {  // CTAs on an SM at a time
       cudaGetLastError();
       n = 0;
     }
-    return std::max(n, 1);
-  }();
-  return ctas;
+    return n;
+  }));
 }
 
 template <int KVM, int D, int W>

@@ -385,19 +385,19 @@ constexpr int smem_bytes() {
   return (ROWS ? kWarps * kRows * D * 2 : (kWarps + 1) * kRows * D) * (int)sizeof(float);
 }
 
-// CTAs resident on an SM at a time (one tile per CTA).
+// CTAs resident on an SM of the current device at a time (one tile per CTA).
 template <int D>
 int resident() {
-  static const int ctas = [] {
+  static PerDevice ctas;
+  return std::max(1, ctas.get(current_device(), [] {
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false>, kWarps * 32,
                                                       smem_bytes<D, false>()) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
-    return std::max(n, 1);
-  }();
-  return ctas;
+    return n;
+  }));
 }
 
 template <int D, bool ROWS>

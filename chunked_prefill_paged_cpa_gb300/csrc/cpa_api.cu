@@ -17,17 +17,15 @@ bool step_path(int dtype, int D, int G) {
 }
 
 int sm_count(int device) {
-  static int sms[64] = {};
-  if (device < 0 || device >= 64) return 0;
-  if (!sms[device]) {
+  static PerDevice sms;
+  return sms.get(device, [&] {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
-    sms[device] = n;
-  }
-  return sms[device];
+    return n;
+  });
 }
 
 WorkspaceLayout workspace_layout(const cpa_desc &d, int num_seqs) {

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "cpa.h"
+#include "per_device.cuh"
 
 namespace cpa {
 
@@ -167,6 +168,12 @@ int check_shape(const cpa_desc *d);
 
 // Number of SMs of a device (cached); 0 if it cannot be queried.
 int sm_count(int device);
+
+// The current device, -1 if it cannot be queried.
+inline int current_device() {
+  int device = -1;
+  return cudaGetDevice(&device) == cudaSuccess ? device : -1;
+}
 
 // The step kernel (attn_step.cuh, one translation unit per cache mode):
 // 16-bit queries, head_dim 64/128, GQA group 1/2/4/8.  KVM 0: bf16 queries and
