@@ -218,10 +218,10 @@ int cpa_append_attention_forward(const void *q, const void *k, const void *v,
  *  - fp32 activations keep fp32's precision: the tensor cores multiply each
  *    operand as the sum of two tf32 values, the products' error is below
  *    2^-21 (cpa_attention_forward rounds a chunk's operands to tf32).  There a
- *    non-finite q, K or V that a row sees gives non-finite outputs, NaN where
- *    the formula's value is infinite or does not depend on it any more; a
- *    magnitude of (2 - 2^-11) 2^127 and more, which is infinite in tf32, counts
- *    as not finite. */
+ *    non-finite q, K or V that a row sees gives non-finite outputs: NaN
+ *    where the formula's value is infinite, and where it is finite because the
+ *    key's score is -infinity.  A magnitude of (2 - 2^-11) 2^127 and more, which is
+ *    infinite in tf32, counts as not finite. */
 int cpa_window_attention_forward(const void *q, const void *k_cache, const void *v_cache,
                                  const int32_t *block_table, const int32_t *query_start_loc,
                                  const int32_t *seq_lens, int32_t num_seqs, float scale,
