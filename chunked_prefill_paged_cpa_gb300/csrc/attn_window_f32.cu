@@ -131,7 +131,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     ctx = cap;
   }
   const int first = (z - (qs / TM + s)) * TM;  // the CTA's first token of the sequence
-  if (qs < 0 || first < 0 || first >= q_len) return;  // (the whole cluster)
+  if (qs < 0 || first < 0 || first >= q_len) {
+    // (the whole cluster; in a malformed batch every one, and what comes next on
+    // the stream must still find the append done)
+    ptx::grid_dependency_wait();
+    return;
+  }
 
   for (int i = threadIdx.x; i < TILES * KS * 32; i += kWarps * 32) {
     const int tile = i / (KS * 32), ks = i / 32 % KS, l = i % 32;

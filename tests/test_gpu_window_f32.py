@@ -62,3 +62,29 @@ def test_precision(cuda_device, shape, d):
     want, _ = reference(b)
     err = (window_call(b, workspace(b)).double() - want).norm() / want.norm()
     assert err < 2.0 ** -19
+
+
+@pytest.mark.parametrize("q_lens,seq_lens", [([0], [1]), ([0, 0, 0], [5, 0, 9])])
+def test_the_append_is_done_behind_a_batch_without_rows(cuda_device, q_lens, seq_lens):
+    """A malformed step (tokens, and no row that owns one): nothing is computed, and what follows on the stream finds every
+    new row in the cache."""
+    tokens, hkv, d = 60_000, 8, 128
+    g = torch.Generator(cuda_device).manual_seed(1)
+    draw = lambda h: torch.randn(tokens, h, d, generator=g, device=cuda_device)  # noqa: E731
+    q, k, v = draw(hkv), draw(hkv), draw(hkv)
+    pages = tokens // 16
+    caches = [torch.full((pages, hkv, 16, d), float("nan"), device=cuda_device) for _ in range(2)]
+    slots = torch.randperm(tokens, generator=g, device=cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    table = torch.arange(len(q_lens) * 8, device=cuda_device).int().view(-1, 8)
+    ws = ops.workspace_for(caches[0], hkv, 8, len(q_lens), tokens)
+    out = torch.full_like(q, 7)
+    for _ in range(3):
+        for c in caches:
+            c.fill_(float("nan"))
+        ops.append_window_attention_forward(q, k, v, slots, *caches, table, i32([0] * (len(q_lens) + 1)), i32(seq_lens), 0.1, ws, 40, 4,
+                                            out=out)
+        got = [c + 0 for c in caches]  # right behind the call
+        for c, x in zip(got, (k, v)):
+            assert torch.equal(c[slots // 16, :, slots % 16], x)
+        assert (out == 7).all()
