@@ -344,19 +344,24 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
     else s_base[s] += 1;
   }
   __syncthreads();
-  // A3: exclusive sums, new pages low, copies high
+  // A3: exclusive sums, new pages in the low 40 bits, copies above: 4096 rows need
+  // at most 2^38 pages, where their tokens overlap (a malformed step).  A row's
+  // sum is kept in 32 bits: it is used where all fit into the pool.
+  constexpr int kCopyShift = 40;
+  constexpr int64_t kPagesMask = ((int64_t)1 << kCopyShift) - 1;
   const int per = div_up(S, kExtThreads);
   const int sa = min(S, tid * per), sb = min(S, sa + per);
   int64_t mine = 0;
-  for (int s = sa; s < sb; ++s) mine += s_base[s] + ((int64_t)(s_head[s] >= 0) << 32);
+  for (int s = sa; s < sb; ++s) mine += s_base[s] + ((int64_t)(s_head[s] >= 0) << kCopyShift);
   int64_t sum = 0, at = block_scan(mine, warps, sum);
   for (int s = sa; s < sb; ++s) {
     const int n = s_base[s], copy = s_head[s] >= 0;
-    s_base[s] = (int)(at & 0xffffffff);
-    s_copy[s] = (int)(at >> 32);
-    at += n + ((int64_t)copy << 32);
+    s_base[s] = (int)(at & kPagesMask);
+    s_copy[s] = (int)(at >> kCopyShift);
+    at += n + ((int64_t)copy << kCopyShift);
   }
-  const int needed = (int)(sum & 0xffffffff), copies = (int)(sum >> 32);
+  const int64_t needed = sum & kPagesMask;
+  const int copies = (int)(sum >> kCopyShift);
 
   // B: the lowest free pages, in turns of 16 K pages per CTA (skipped where
   // nothing is needed)
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(kExtThreads) extend_kernel(const ExtendArgs a)
   const bool fits = have >= needed;
   if (rank == 0 && tid == 0) {
     a.counts[0] = fits ? copies : 0;
-    a.counts[1] = fits ? needed : -needed;
+    a.counts[1] = (int)(fits ? needed : -min(needed, (int64_t)INT32_MAX));
     if (!fits) atomicOr(a.status, STATUS_NO_PAGES);
   }
   // entry *e becomes the r-th free page; what it held is noted in its place

@@ -308,8 +308,8 @@ int cpa_fork_sequences(const int32_t *parents, const int32_t *children, int32_t 
  * The pairs have to be copied (cpa_copy_pages with num_pairs = counts, in every
  * layer's cache) before the step's rows are appended.
  * If fewer pages are free than the step needs, nothing is changed: every
- * slot_mapping entry is -1, counts = {0, -needed}, and the status word is
- * raised.  (The attention calls take rows with tokens only: a caller whose rows
+ * slot_mapping entry is -1, counts = {0, -needed} (at least -2^31 + 1), and the
+ * status word is raised.  (The attention calls take rows with tokens only: a caller whose rows
  * sit steps out gathers the others' block_table, query_start_loc and seq_lens.)
  * A row with q_len < 0, seq_lens[s] < q_len, more tokens than its
  * block_table row or than desc->num_tokens can hold takes nothing, its tokens'
