@@ -516,6 +516,10 @@ bool window_decode_takes(const AttnParams &p, int sms) {
 // 48 / 48 us, 32 tokens (111 pages per SM) 54 / 64, 64 tokens 60 / 93; window 4096
 // and 16 tokens 104 / 134.  16-bit caches gain little (64 tokens 78 / 82 us) and
 // lose it again on a cold start: they stay in the step kernel's queue.
+// (Whether clusters fill the SMs is asked of all the step's tokens.  Asked of its
+// sequences alone, 8-bit caches of 1 kv head, window 65536 beside 480 tokens:
+// 4 tokens 242 / 293 us, 8 tokens 275 / 239 us, 16 tokens 318 / 293 us; of 2 kv
+// heads, 4 tokens 391 / 484 us, 7 tokens 392 / 375 us.)
 bool window_decode_beside(const AttnParams &p, int sms) {
   constexpr int kLeastPages = 96;  // per SM
   return p.kv_e4m3 && window_decode_takes(p, sms) &&
