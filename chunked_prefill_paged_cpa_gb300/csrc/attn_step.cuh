@@ -56,7 +56,7 @@
 // v_scale into the output.  The widening also zeroes the rows of cache slots
 // past the sequence.
 //
-// Sliding window with sinks (template WIN): the row at position x sees the keys
+// Sliding window with sinks (template VIS = kWindow): the row at position x sees the keys
 // j <= x with j < sinks or j > x - window.  The rows of one item between them
 // see the pages of the sinks and the pages from the first row's window to the
 // last row, two runs of the block table.  The item's keys are numbered through
@@ -69,8 +69,15 @@
 // visible keys cost, whatever the length of the sequences: pages outside are
 // neither read nor looked up (their entries may be anything, freed pages say).
 //
-// This header is compiled once per cache mode (attn_step_<mode>.cu), and once
-// more with the window (attn_window_<mode>.cu).
+// Selected pages (VIS = kSelected): the rows of a tile pair, or a decode, see the
+// pages listed for them and their own from page L on, which the position of the
+// first row gives (unit_limit).  The numbering is that of the window with the list in the
+// sinks' place: virtual page v is page list[v], or v + gap behind the list.  The
+// list's length follows from L alone, so the plan needs none of its entries.
+//
+// This header is compiled once per cache mode (attn_step_<mode>.cu), once
+// more with the window (attn_window_<mode>.cu), and with the lists
+// (attn_selected_<mode>.cu).
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -188,22 +195,24 @@ __device__ __forceinline__ int tile_kv(int ctx, int q_len, int m) {
 
 // Pages that an item leaves out between the sinks and its first row's window
 // (its first row at position x): virtual page v is page v + gap behind the sinks.
-template <bool WIN>
+// (Selected pages: between the list and its page L.)
+template <int VIS>
 __device__ __forceinline__ int gap_pages(const AttnParams &p, int x) {
-  if (!WIN) return 0;
+  if (VIS == kAll) return 0;
+  if (VIS == kSelected) return max(0, unit_limit(p, x) - p.budget);
   return max(0, max(0, x - p.window + 1) / kPage - ceil_div(p.sinks, kPage));
 }
 
 // Context of a decode in virtual positions.
-template <bool WIN>
+template <int VIS>
 __device__ __forceinline__ int decode_ctx(const AttnParams &p, int ctx) {
-  return ctx - kPage * gap_pages<WIN>(p, ctx - 1);
+  return ctx - kPage * gap_pages<VIS>(p, ctx - 1);
 }
 
 // KV tiles of tile pair mp of a chunk (mt query tiles).
-template <int G, bool WIN>
+template <int G, int VIS>
 __device__ __forceinline__ int pair_kv(const AttnParams &p, int ctx, int q_len, int mp, int mt) {
-  const int gap = gap_pages<WIN>(p, ctx - q_len + 2 * mp * (BM / G));
+  const int gap = gap_pages<VIS>(p, ctx - q_len + 2 * mp * (BM / G));
   return tile_kv<G>(ctx - kPage * gap, q_len, min(2 * mp + 1, mt - 1));
 }
 
@@ -236,7 +245,7 @@ __host__ __device__ __forceinline__ int64_t plan_q_pieces(const AttnParams &p) {
   return (KVM == 2 && !p.act_f16) ? (int64_t)p.num_tokens * p.Hq * (p.D * 2 / 16) : 0;
 }
 
-template <int KVM, int G, bool WIN>
+template <int KVM, int G, int VIS>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p,
                                                                   const StepWs w) {
   // the step kernel may be scheduled now: it waits in grid_dependency_wait
@@ -318,23 +327,23 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     const int qs = __ldg(p.query_start_loc + s);
     int q_len = __ldg(p.query_start_loc + s + 1) - qs;
     // single tokens that a kernel of their own computes beside this one
-    if (WIN && q_len == 1 && p.rows_mode == 1) q_len = 0;
+    if (VIS != kAll && q_len == 1 && p.rows_mode == 1) q_len = 0;
     const int ctx = q_len < 1 ? 0 : seq_ctx(p, s, q_len);
     sq_qs[s] = qs;
     sq_len[s] = q_len;
     sq_ctx[s] = ctx;
     if (q_len == 1) {
-      pages += (long long)Hkv * ceil_div(decode_ctx<WIN>(p, ctx), kPage);
+      pages += (long long)Hkv * ceil_div(decode_ctx<VIS>(p, ctx), kPage);
     } else if (q_len > 1) {
       const int mt = ceil_div(q_len * G, BM), npair = (mt + 1) / 2;
       pairs += (long long)Hkv * npair;
       // tiles per pair grow about linearly from the first pair to the last, or
       // until they fill the window: one more sample, in the middle
-      const int t0 = pair_kv<G, WIN>(p, ctx, q_len, 0, mt);
-      const int t1 = pair_kv<G, WIN>(p, ctx, q_len, npair - 1, mt);
-      if (WIN)
+      const int t0 = pair_kv<G, VIS>(p, ctx, q_len, 0, mt);
+      const int t1 = pair_kv<G, VIS>(p, ctx, q_len, npair - 1, mt);
+      if (VIS != kAll)
         ctiles += (long long)Hkv * npair *
-                  (t0 + 2 * pair_kv<G, WIN>(p, ctx, q_len, npair / 2, mt) + t1) / 4;
+                  (t0 + 2 * pair_kv<G, VIS>(p, ctx, q_len, npair / 2, mt) + t1) / 4;
       else
         ctiles += (long long)Hkv * npair * (t0 + t1) / 2;
     }
@@ -369,9 +378,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
       (int)max((long long)kMinUnitTiles, ((tt + (tp + 7) / 8 + grid - 1) / grid * 3 + 3) / 4);
   auto units = [&](int s) {  // chunk units of one kv head of sequence s
     const int mt = ceil_div(sq_len[s] * G, BM), npair = (mt + 1) / 2;
-    return npair * min(nu, ceil_div(pair_kv<G, WIN>(p, sq_ctx[s], sq_len[s], npair - 1, mt), unit_tiles));
+    return npair * min(nu, ceil_div(pair_kv<G, VIS>(p, sq_ctx[s], sq_len[s], npair - 1, mt), unit_tiles));
   };
-  auto dec_pages = [&](int s) { return ceil_div(decode_ctx<WIN>(p, sq_ctx[s]), kPage); };
+  auto dec_pages = [&](int s) { return ceil_div(decode_ctx<VIS>(p, sq_ctx[s]), kPage); };
   auto pieces = [&](int s) { return ceil_div(dec_pages(s), P); };
   auto bucket = [&](int s) {  // size class of a decode sequence's pieces, in blocks
     const int n = dec_pages(s);
@@ -563,7 +572,7 @@ __device__ __forceinline__ uint16_t cvt_out(float a, bool f16) {
 // second half of the rows at D = 64): taken a group of rows at a time, in
 // order, a group's stores land only on its own codes (read before the
 // __syncwarp) or on those of groups already done.
-template <int D, bool WIN>
+template <int D, int VIS>
 __device__ __forceinline__ void widen_page(const unsigned char *src, unsigned char *dst,
                                            int pstride, int zrow, int z0, int z1, int lane) {
   constexpr int CPR = D / 16;       // 16-byte chunks of codes per row
@@ -578,7 +587,7 @@ __device__ __forceinline__ void widen_page(const unsigned char *src, unsigned ch
     ptx::e4m3x4_to_f16x4(in.y, w[2], w[3]);
     ptx::e4m3x4_to_f16x4(in.z, w[4], w[5]);
     ptx::e4m3x4_to_f16x4(in.w, w[6], w[7]);
-    if (rr >= zrow || (WIN && rr >= z0 && rr < z1)) {
+    if (rr >= zrow || (VIS == kWindow && rr >= z0 && rr < z1)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 0u;
     }
@@ -606,18 +615,23 @@ __device__ __forceinline__ void fill_of(int f, int n, bool &is_v, int &t) {
 // Keys from here on no row of the item sees: the cache slots past the sequence
 // (of `ctx` positions) and, with a window, the tokens of a chunk behind the last
 // row of tile pair mp.
-template <int G, bool WIN>
+template <int G, int VIS>
 __device__ __forceinline__ int item_end(int ctx, int q_len, int mp) {
-  return WIN ? min(ctx, ctx - q_len + 2 * (mp + 1) * (BM / G)) : ctx;
+  return VIS != kAll ? min(ctx, ctx - q_len + 2 * (mp + 1) * (BM / G)) : ctx;
+}
+
+// Position of an item's first row.
+template <int G>
+__device__ __forceinline__ int item_first(const ItemDesc &d) {
+  return (d.s_kind >> 30) == KIND_DECODE ? d.ctx - 1 : d.ctx - d.q_len + 2 * (d.g_x >> 8) * (BM / G);
 }
 
 // Derive an item's geometry from its queue entry (every lane computes the same).
 // Returns the pages left out behind the sinks; the item's positions are virtual.
-template <int D, int G, bool WIN>
+template <int D, int G, int VIS>
 __device__ __forceinline__ int derive_item(const AttnParams &p, const ItemDesc &d, WorkItem &it) {
-  constexpr int TM = BM / G;
   const bool dec = (d.s_kind >> 30) == KIND_DECODE;
-  const int gap = gap_pages<WIN>(p, dec ? d.ctx - 1 : d.ctx - d.q_len + 2 * (d.g_x >> 8) * TM);
+  const int gap = gap_pages<VIS>(p, item_first<G>(d));
   const int ctx = d.ctx - kPage * gap;
   it.s = d.s_kind & 0x3fffffff;
   it.qs = d.qs;
@@ -658,7 +672,7 @@ __device__ __forceinline__ int derive_item(const AttnParams &p, const ItemDesc &
     // (pages past the last are not read: their keys and values are zeros.  8192
     // tokens, window 2048: 240.9 us; with those pages read, and their V rows zeroed
     // by the softmax warps, 248.2 us; neither, which lets NaN through, 240.0 us)
-    it.n_pages = ceil_div(item_end<G, WIN>(ctx, d.q_len, it.mp), kPage);
+    it.n_pages = ceil_div(item_end<G, VIS>(ctx, d.q_len, it.mp), kPage);
     it.page_end = it.n_pages;
     it.nsplit = nu;
     it.slot = d.b;
@@ -709,7 +723,7 @@ struct VRing {
   }
 };
 
-template <int KVM, int D, int G, bool WIN>
+template <int KVM, int D, int G, int VIS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_qd, const __grid_constant__ CUtensorMap tm_k,
@@ -765,7 +779,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
   ptx::grid_dependency_wait();
   // (a kernel launched behind this one, for the single tokens, may take the SMs
   // that this grid leaves)
-  if (WIN) ptx::grid_launch_dependents();
+  if (VIS != kAll) ptx::grid_launch_dependents();
   const int n_items = __ldcg(w.hdr + 2);
 
   if (warp == kProducerWarp) {
@@ -824,7 +838,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       WorkItem it;
       int gap = 0;
       if (have) {
-        gap = derive_item<D, G, WIN>(p, dsc, it);
+        gap = derive_item<D, G, VIS>(p, dsc, it);
         if (it.n_tiles == 0) {  // a unit with no keys in its range
           have = fetch(claim(), dsc);
           continue;
@@ -881,11 +895,27 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       // holds page wb + 32 b + l of window b), the next window prefetched
       const int32_t *bt = p.block_table + (int64_t)it.s * p.max_pages;
       const int wb = it.page0 + 8 * it.j0;
-      const int sink_pages = WIN ? ceil_div(p.sinks, kPage) : 0;
+      // virtual pages before the gap: the sinks', or the list of the item's first token
+      int front = VIS == kWindow ? ceil_div(p.sinks, kPage) : 0;
+      const int32_t *listed = nullptr;
+      if (VIS == kSelected) {
+        const int t0 = it.qs + (it.kind == KIND_CHUNK ? 2 * it.mp * TM : 0);
+        const int limit = unit_limit(p, item_first<G>(dsc));
+        front = min(limit, p.budget);
+        if (t0 >= 0 && t0 < p.num_tokens) listed = p.selected + ((int64_t)t0 * p.Hkv + it.g) * p.budget;
+      }
       auto load_window = [&](int b) -> int {
         const int pi = wb + 32 * b + lane;
         if (pi >= it.page_end) return kv_rows;  // past the item: zero fill
-        const int page = __ldg(bt + (WIN && pi >= sink_pages ? pi + gap : pi));
+        int col = VIS != kAll && pi >= front ? pi + gap : pi;
+        if (VIS == kSelected && pi < front) {
+          col = listed ? __ldg(listed + pi) : -1;
+          if (col < 0 || col >= front + gap) {
+            atomicOr(p.status, STATUS_BAD_PAGE);
+            return kv_rows;
+          }
+        }
+        const int page = __ldg(bt + col);
         if (page < 0 || page >= p.num_pages) {
           atomicOr(p.status, STATUS_BAD_PAGE);
           return kv_rows;
@@ -1082,7 +1112,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
               unlock();
               ptx::mma_commit(&bs->s_full[ti]);
               ptx::mma_commit(&bs->k_empty[kvm % C::KST]);
-              if (WIN && n_mine == 1) ptx::mma_commit(&bs->q_empty[qb]);
+              if (VIS != kAll && n_mine == 1) ptx::mma_commit(&bs->q_empty[qb]);
             }
           }
           for (int j = 0; ok && j < n_mine; ++j) {
@@ -1114,7 +1144,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
               // the tile's last Q K^T: the next item's queries may load while the
               // last tile's softmax, its P V and the epilogue still run (prefill of
               // 8192 tokens, window 2048: 250 -> 239 us)
-              if (WIN && j + 2 == n_mine) ptx::mma_commit(&bs->q_empty[qb]);
+              if (VIS != kAll && j + 2 == n_mine) ptx::mma_commit(&bs->q_empty[qb]);
             } else {
               ptx::mma_commit(&bs->o_final[ti]);
             }
@@ -1244,7 +1274,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           if (ok) ok = observe_through(2 * nt - 1);
         }
         if (ok) {
-          if (WIN && !dec && n_mine > 0) {
+          if (VIS != kAll && !dec && n_mine > 0) {
             // (committed behind the last Q K^T)
           } else if (n_mine > 0) {
             ptx::mma_commit(&bs->q_empty[qb]);
@@ -1295,10 +1325,10 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       // With a window: keys z0 .. z1 - 1 lie behind the sinks and before the
       // window of the item's first row, in the pages that hold those edges.  No
       // row sees them; their V rows are zeroed, since 0 * NaN is NaN inside PV.
-      const int z0 = WIN ? p.sinks : 0;
-      const int z1 = WIN ? (it.kind == KIND_CHUNK ? ctx - it.q_len + 2 * it.mp * TM : ctx - 1) - p.window + 1 : 0;
+      const int z0 = VIS == kWindow ? p.sinks : 0;
+      const int z1 = VIS == kWindow ? (it.kind == KIND_CHUNK ? ctx - it.q_len + 2 * it.mp * TM : ctx - 1) - p.window + 1 : 0;
       // The same holds from `end` on, in the page that holds it.
-      const int end = WIN && it.kind == KIND_CHUNK ? item_end<G, WIN>(ctx, it.q_len, it.mp) : ctx;
+      const int end = VIS != kAll && it.kind == KIND_CHUNK ? item_end<G, VIS>(ctx, it.q_len, it.mp) : ctx;
       vr.begin(it.kind);
       // E4M3 cache: widen the item's fills, in the producer's order, up to
       // fill `last` (this warp: page `warp` of each tile).  Every softmax warp
@@ -1329,10 +1359,10 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           if (!__all_sync(0xffffffffu, ptx::mbar_wait(full, par))) return false;
           const int key0 = (it.page0 + 8 * (it.j0 + t) + warp) * kPage;  // this page's first key
           if (is_v)
-            widen_page<D, WIN>(stage + warp * C::PAGE_BYTES + C::V8_OFF, stage + warp * C::PAGE_BYTES,
+            widen_page<D, VIS>(stage + warp * C::PAGE_BYTES + C::V8_OFF, stage + warp * C::PAGE_BYTES,
                                kPage * 128, end - key0, z0 - key0, z1 - key0, lane);
           else
-            widen_page<D, WIN>(stage + warp * kPage * 128 + C::K8_OFF, stage + warp * kPage * 128,
+            widen_page<D, VIS>(stage + warp * kPage * 128 + C::K8_OFF, stage + warp * kPage * 128,
                                BN * 128, end - key0, z0 - key0, z1 - key0, lane);
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(conv);
@@ -1355,10 +1385,10 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           const int nvis = last - key0 + 1;        // visible keys of this row in the tile
           // with a window: the row's sinks end, and its window begins, at
           // these columns of the tile
-          const int wa = WIN ? p.sinks - key0 : 0, wb = WIN ? last - p.window + 1 - key0 : 0;
-          const bool edge = WIN && wb > 0 && wa < BN;
+          const int wa = VIS == kWindow ? p.sinks - key0 : 0, wb = VIS == kWindow ? last - p.window + 1 - key0 : 0;
+          const bool edge = VIS == kWindow && wb > 0 && wa < BN;
           auto mask = [&](uint32_t (&x)[32], int c0) {
-            if (WIN) {
+            if (VIS == kWindow) {
               if (diag || edge) mask_window(x, nvis - c0, wa - c0, wb - c0);
             } else if (diag) {
               mask_chunk(x, nvis - c0);
@@ -1418,15 +1448,15 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           // Cache slots at or past `end` may hold anything (NaN included) and
           // 0 * NaN is NaN inside PV: zero those V rows first (an E4M3 cache:
           // already zeroed by the widening).
-          if (KVM != 2 && ((key0 + BN > end && (!WIN || end % kPage)) ||
-                           (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
+          if (KVM != 2 && ((key0 + BN > end && (VIS == kAll || end % kPage)) ||
+                           (VIS == kWindow && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
             const int vst = vr.stage(j);
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bs->v_full[vst], vr.use(j) & 1))) {
               ok = false;
               break;
             }
             if ((r >= end - key0 && r < it.n_pages * kPage - key0) ||
-                (WIN && r >= z0 - key0 && r < z1 - key0)) {
+                (VIS == kWindow && r >= z0 - key0 && r < z1 - key0)) {
               unsigned char *vrow = v_stage(vst) + (r / kPage) * C::PAGE_BYTES + (r % kPage) * 128;
 #pragma unroll
               for (int pl = 0; pl < C::PANELS; ++pl)
@@ -1571,7 +1601,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           uint32_t sr[G];
           ptx::tmem_ld_cols<G>(tS, sr);
           const int key = (it.page0 + 8 * blk) * kPage + r;
-          const bool valid = key < key_lim && (!WIN || key < z0 || key >= z1);
+          const bool valid = key < key_lim && (VIS != kWindow || key < z0 || key >= z1);
           float sv[G];
 #pragma unroll
           for (int q = 0; q < G; ++q) {
@@ -1614,14 +1644,14 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           // (an E4M3 cache: already zeroed by the widening)
           const int key0 = (it.page0 + 8 * blk) * kPage;
           if (KVM != 2 && ((key0 + BN > ctx && key0 < it.n_pages * kPage) ||
-                           (WIN && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
+                           (VIS == kWindow && z0 < z1 && z1 > key0 && z0 < key0 + BN))) {
             const int vst = vr.stage(blk);
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bs->v_full[vst], vr.use(blk) & 1))) {
               ok = false;
               break;
             }
             if ((key >= ctx && key < min(it.n_pages, it.page_end) * kPage) ||
-                (WIN && key >= z0 && key < z1)) {
+                (VIS == kWindow && key >= z0 && key < z1)) {
               unsigned char *vrow = v_stage(vst) + (r / kPage) * C::PAGE_BYTES + (r % kPage) * 128;
 #pragma unroll
               for (int pl = 0; pl < C::PANELS; ++pl)
@@ -1779,7 +1809,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-template <int KVM, int D, int G, bool WIN>
+template <int KVM, int D, int G, int VIS>
 cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream) {
   using C = StepCfg<D>;
   auto encode = encode_fn();
@@ -1860,7 +1890,7 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   cudaError_t e = cudaSuccess;
   static PerDevice configured;
   if (configured.get(device, [&] {
-        e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G, WIN>,
+        e = cudaFuncSetAttribute(attn_step_kernel<KVM, D, G, VIS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         return e == cudaSuccess ? 1 : 0;
       }) < 1)
@@ -1870,13 +1900,13 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   const int side_ctas = (int)std::min<int64_t>(w.grid, (side + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
   static PerDevice plan_configured;
   if (plan_configured.get(device, [&] {
-        e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G, WIN>,
+        e = cudaFuncSetAttribute(attn_plan_kernel<KVM, G, VIS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)plan_smem_bytes(kDecodeMaxSeqs));
         return e == cudaSuccess ? 1 : 0;
       }) < 1)
     return e;
-  attn_plan_kernel<KVM, G, WIN><<<1 + side_ctas, kPlanThreads, plan_smem_bytes(p.num_seqs), stream>>>(p, w);
+  attn_plan_kernel<KVM, G, VIS><<<1 + side_ctas, kPlanThreads, plan_smem_bytes(p.num_seqs), stream>>>(p, w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // ... then the step, allowed to start while the plan finishes
@@ -1890,27 +1920,27 @@ cudaError_t launch_dg(const AttnParams &p, const StepWs &w, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_step_kernel<KVM, D, G, WIN>, p, w, tq, tqd, tk, tv, (int)rows);
+  return cudaLaunchKernelEx(&cfg, attn_step_kernel<KVM, D, G, VIS>, p, w, tq, tqd, tk, tv, (int)rows);
 }
 
 }  // namespace
 
-template <int KVM, bool WIN>
+template <int KVM, int VIS>
 cudaError_t launch_step(const AttnParams &p, const StepWs &w, cudaStream_t stream) {
   const int G = p.Hq / p.Hkv;
   if (p.D == 128) {
     switch (G) {
-      case 1: return launch_dg<KVM, 128, 1, WIN>(p, w, stream);
-      case 2: return launch_dg<KVM, 128, 2, WIN>(p, w, stream);
-      case 4: return launch_dg<KVM, 128, 4, WIN>(p, w, stream);
-      case 8: return launch_dg<KVM, 128, 8, WIN>(p, w, stream);
+      case 1: return launch_dg<KVM, 128, 1, VIS>(p, w, stream);
+      case 2: return launch_dg<KVM, 128, 2, VIS>(p, w, stream);
+      case 4: return launch_dg<KVM, 128, 4, VIS>(p, w, stream);
+      case 8: return launch_dg<KVM, 128, 8, VIS>(p, w, stream);
     }
   } else {
     switch (G) {
-      case 1: return launch_dg<KVM, 64, 1, WIN>(p, w, stream);
-      case 2: return launch_dg<KVM, 64, 2, WIN>(p, w, stream);
-      case 4: return launch_dg<KVM, 64, 4, WIN>(p, w, stream);
-      case 8: return launch_dg<KVM, 64, 8, WIN>(p, w, stream);
+      case 1: return launch_dg<KVM, 64, 1, VIS>(p, w, stream);
+      case 2: return launch_dg<KVM, 64, 2, VIS>(p, w, stream);
+      case 4: return launch_dg<KVM, 64, 4, VIS>(p, w, stream);
+      case 8: return launch_dg<KVM, 64, 8, VIS>(p, w, stream);
     }
   }
   return cudaErrorInvalidValue;

@@ -2,5 +2,5 @@
 #include "attn_step.cuh"
 
 namespace cpa {
-template cudaError_t launch_step<0, false>(const AttnParams &, const StepWs &, cudaStream_t);
+template cudaError_t launch_step<0, kAll>(const AttnParams &, const StepWs &, cudaStream_t);
 }  // namespace cpa

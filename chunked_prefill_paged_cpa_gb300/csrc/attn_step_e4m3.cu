@@ -2,5 +2,5 @@
 #include "attn_step.cuh"
 
 namespace cpa {
-template cudaError_t launch_step<2, false>(const AttnParams &, const StepWs &, cudaStream_t);
+template cudaError_t launch_step<2, kAll>(const AttnParams &, const StepWs &, cudaStream_t);
 }  // namespace cpa

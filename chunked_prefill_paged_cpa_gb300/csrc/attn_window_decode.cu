@@ -1,8 +1,8 @@
-// Windowed attention of a batch of single tokens, 16-bit queries: one launch, no
-// plan.
+// Attention of a batch of single tokens that see a window, or selected pages, with
+// 16-bit queries: one launch, no plan.
 //
-// With a window, every row sees about the same number of keys and the host
-// knows a bound on it, so the step kernel's queue has nothing to balance.  Work
+// Either way every row sees about the same number of keys and the host knows a
+// bound on it, so the step kernel's queue has nothing to balance.  Work
 // is split evenly instead: a cluster of CTAs per (token, kv head), its warps
 // taking equal runs of the row's pages.  Per page of 16 keys a warp runs
 //   S = K Q^T      m16n8k16, keys x the G heads of the group (padded to 8)
@@ -115,7 +115,7 @@ struct PageRegs {
   }
 };
 
-template <int KVM, int D, int W>
+template <int KVM, int D, int W, int VIS>
 __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams p) {
   constexpr bool F16 = KVM != 0;
   constexpr int EB = KVM == 2 ? 1 : 2;
@@ -155,12 +155,25 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
     if (threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_PAGE);
     ctx = cap;
   }
-  // keys [0, near) and [far, vis); page v of the row's pages is block-table
-  // column v, or v + gap behind the sinks
+  // kWindow: keys [0, near) and [far, vis); page v of the row's pages is
+  // block-table column v, or v + gap behind the `front` pages of the sinks.
+  // kSelected: keys [far, vis) and whole pages; the front pages are columns listed[v].
   const int vis = t - qs < q_len ? max(0, ctx - q_len + (t - qs) + 1) : 0;
-  const int far = max(0, vis - p.window), near = min(p.sinks, far);
-  const int sink_pages = (near + kPageKeys - 1) / kPageKeys;
-  const int gap = max(0, far / kPageKeys - sink_pages);
+  int far, near, front;
+  const int32_t *listed = nullptr;
+  if constexpr (VIS == kSelected) {
+    const int unit = (t - qs) / (kUnitRows / G) * (kUnitRows / G);  // 0: a token of its own
+    const int limit = unit_limit(p, max(0, vis - 1 - (t - qs - unit)));
+    far = limit * kPageKeys;
+    front = qs + unit < 0 || qs + unit >= p.num_tokens ? 0 : min(limit, p.budget);  // (0: a malformed batch)
+    near = front * kPageKeys;
+    listed = p.selected + ((int64_t)(qs + unit) * p.Hkv + g) * p.budget;
+  } else {
+    far = max(0, vis - p.window);
+    near = min(p.sinks, far);
+    front = (near + kPageKeys - 1) / kPageKeys;
+  }
+  const int gap = max(0, far / kPageKeys - front);
   const int np = (vis + kPageKeys - 1) / kPageKeys - gap;
   const int wi = rank * W + warp, nw = nc * W;
   const int v0 = (int)((int64_t)np * wi / nw), v1 = (int)((int64_t)np * (wi + 1) / nw);
@@ -197,7 +210,12 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
     entry = -1;
     if (base + lane < v1) {
       const int v = base + lane;
-      entry = __ldg(bt + (v < sink_pages ? v : v + gap));
+      int col = v < front ? v : v + gap;
+      if (VIS == kSelected && v < front) {
+        col = __ldg(listed + v);
+        if (col >= front + gap) col = -1;  // not one of the list's candidates
+      }
+      if (VIS != kSelected || col >= 0) entry = __ldg(bt + col);
       if (entry < 0 || entry >= p.num_pages) {
         atomicOr(p.status, STATUS_BAD_PAGE);
         entry = -1;
@@ -242,7 +260,9 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
     for (int i = 0; i < 4; ++i) sc[i] = (sa[i] + sb[i]) * sl2;
     // pages at the edges of what the row sees: other keys get no weight, and
     // their V, which may hold anything, becomes zero
-    const int key0 = (v < sink_pages ? v : v + gap) * kPageKeys;
+    // (a listed page's keys are all seen: its place among the front pages stands
+    // for its column)
+    const int key0 = (v < front ? v : v + gap) * kPageKeys;
     if (e < 0 || key0 + kPageKeys > vis || (key0 < far && key0 + kPageKeys > near)) {
       auto seen = [&](int k) { return e >= 0 && k < vis && (k < near || k >= far); };
       if (!seen(key0 + r)) sc[0] = sc[1] = -INFINITY;
@@ -426,11 +446,12 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
 
 // Pages that a row sees at most.
 int64_t page_bound(const AttnParams &p) {
+  if (p.vis == kSelected) return std::min<int64_t>(p.max_pages, (int64_t)p.budget + p.local_pages);
   return std::min<int64_t>(p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 1 +
                                             (p.sinks + kPageKeys - 1) / kPageKeys);
 }
 
-template <int KVM, int D, int W>
+template <int KVM, int D, int W, int VIS>
 int resident() {  // CTAs on an SM of the current device at a time
   static PerDevice ctas;
   return std::max(1, ctas.get(current_device(), [] {
@@ -439,9 +460,9 @@ int resident() {  // CTAs on an SM of the current device at a time
     // with nearly all of it as shared memory, and is to be set up anew.  (64
     // tokens of window 4096 beside a 480-token chunk, 8-bit cache: 192 us without
     // this hint, 151 us with it.)
-    if (cudaFuncSetAttribute(window_decode_kernel<KVM, D, W>,
+    if (cudaFuncSetAttribute(window_decode_kernel<KVM, D, W, VIS>,
                              cudaFuncAttributePreferredSharedMemoryCarveout, 40) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D, W>, W * 32, 0) !=
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_decode_kernel<KVM, D, W, VIS>, W * 32, 0) !=
             cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -450,7 +471,7 @@ int resident() {  // CTAs on an SM of the current device at a time
   }));
 }
 
-template <int KVM, int D, int W>
+template <int KVM, int D, int W, int VIS>
 cudaError_t launch_on(const AttnParams &p, int nc, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc, p.Hkv, p.rows_mode == 2 ? p.num_seqs : p.num_tokens);
@@ -464,23 +485,23 @@ cudaError_t launch_on(const AttnParams &p, int nc, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.rows_mode == 2 || p.fused ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D, W>, p);
+  return cudaLaunchKernelEx(&cfg, window_decode_kernel<KVM, D, W, VIS>, p);
 }
 
-template <int KVM, int D>
+template <int KVM, int D, int VIS>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
   // CTAs per (token, kv head): the number with the fewest rounds of resident
   // CTAs, counted in a warp's pages, a start and a join costing about three
   const int64_t rows = (int64_t)(p.rows_mode == 2 ? p.num_seqs : p.num_tokens) * p.Hkv;
-  const int64_t slots = (int64_t)resident<KVM, D, kWarps>() * sms, pages = page_bound(p);
+  const int64_t slots = (int64_t)resident<KVM, D, kWarps, VIS>() * sms, pages = page_bound(p);
   if constexpr (KVM == 2) {
     // Rows for more than one round, over an 8-bit cache: CTAs of two warps, since
     // starts and joins weigh more beside the shorter pages (256 tokens of 8 kv
     // heads: window 1024 97 / 90 us, 4096 339 / 320 us with four and with two warps;
     // 64 tokens, one round, 85 / 89 us).
     if (rows > slots) {
-      resident<KVM, D, 2>();
-      return launch_on<KVM, D, 2>(p, 1, stream);
+      resident<KVM, D, 2, VIS>();
+      return launch_on<KVM, D, 2, VIS>(p, 1, stream);
     }
   }
   int nc = 1;
@@ -492,7 +513,7 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
       nc = n;
     }
   }
-  return launch_on<KVM, D, kWarps>(p, nc, stream);
+  return launch_on<KVM, D, kWarps, VIS>(p, nc, stream);
 }
 
 }  // namespace
@@ -526,13 +547,19 @@ bool window_decode_beside(const AttnParams &p, int sms) {
          (int64_t)p.num_seqs * p.Hkv * page_bound(p) >= (int64_t)kLeastPages * sms;
 }
 
-cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream) {
+template <int VIS>
+static cudaError_t launch_seeing(const AttnParams &p, int sms, cudaStream_t stream) {
   if (p.D == 128) {
-    if (p.kv_e4m3) return launch<2, 128>(p, sms, stream);
-    return p.act_f16 ? launch<1, 128>(p, sms, stream) : launch<0, 128>(p, sms, stream);
+    if (p.kv_e4m3) return launch<2, 128, VIS>(p, sms, stream);
+    return p.act_f16 ? launch<1, 128, VIS>(p, sms, stream) : launch<0, 128, VIS>(p, sms, stream);
   }
-  if (p.kv_e4m3) return launch<2, 64>(p, sms, stream);
-  return p.act_f16 ? launch<1, 64>(p, sms, stream) : launch<0, 64>(p, sms, stream);
+  if (p.kv_e4m3) return launch<2, 64, VIS>(p, sms, stream);
+  return p.act_f16 ? launch<1, 64, VIS>(p, sms, stream) : launch<0, 64, VIS>(p, sms, stream);
+}
+
+cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream) {
+  return p.vis == kSelected ? launch_seeing<kSelected>(p, sms, stream)
+                            : launch_seeing<kWindow>(p, sms, stream);
 }
 
 }  // namespace cpa

@@ -2,5 +2,5 @@
 #include "attn_step.cuh"
 
 namespace cpa {
-template cudaError_t launch_step<1, true>(const AttnParams &, const StepWs &, cudaStream_t);
+template cudaError_t launch_step<1, kWindow>(const AttnParams &, const StepWs &, cudaStream_t);
 }  // namespace cpa

@@ -1,4 +1,5 @@
-// Windowed attention in fp32: chunks and single tokens, one launch.
+// Attention in fp32 of rows that see a window, or selected pages: chunks and single
+// tokens, one launch.
 //
 // A tile is 16 query rows of one (sequence, kv head): 16 / G consecutive tokens
 // by the G heads of the group (row = token * G + head); a single token fills G
@@ -97,7 +98,7 @@ struct UnitRegs {
   }
 };
 
-template <int D, bool ROWS>
+template <int D, bool ROWS, int VIS>
 __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnParams p) {
   constexpr int KS = D / 8;               // k-steps of S, and 8-dim tiles of O
   constexpr int TILES = ROWS ? kWarps : 1;  // tiles of the CTA
@@ -164,11 +165,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   const int ta = tok0 + r / G, tb = tok0 + (r + 8) / G;
   const int xa = base + ta, xb = base + tb;
   const int x0 = base + tok0, x1 = base + min(tok0 + kRows / G, q_len) - 1;  // first and last
-  // the keys that rows of the tile see: [0, near) and [far, x1]
+  // the keys that rows of the tile see: [0, near) and [far, x1]; kSelected:
+  // [far, x1] and the whole pages listed for the tile's unit
   const bool any = tok0 < q_len && base >= 0;
-  const int far = max(0, x0 - p.window + 1), near = min(p.sinks, far);
-  const int sink_pages = (near + kPageKeys - 1) / kPageKeys;
-  const int gap = max(0, far / kPageKeys - sink_pages);
+  int far, near, front;  // front: virtual pages before the gap
+  const int32_t *listed = nullptr;
+  if constexpr (VIS == kSelected) {
+    const int unit = tok0 / (kUnitRows / G) * (kUnitRows / G);
+    const int limit = unit_limit(p, max(0, base + unit));
+    far = limit * kPageKeys;
+    front = min(limit, p.budget);
+    near = front * kPageKeys;
+    listed = p.selected + ((int64_t)(qs + unit) * p.Hkv + g) * p.budget;
+  } else {
+    far = max(0, x0 - p.window + 1);
+    near = min(p.sinks, far);
+    front = (near + kPageKeys - 1) / kPageKeys;
+  }
+  const int gap = max(0, far / kPageKeys - front);
   const int units = any ? 2 * ((x1 + kPageKeys) / kPageKeys - gap) : 0;
   const int wi = ROWS ? 0 : rank * kWarps + warp, nw = ROWS ? 1 : nc * kWarps;
   const int u0 = (int)((int64_t)units * wi / nw), u1 = (int)((int64_t)units * (wi + 1) / nw);
@@ -184,7 +198,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     entry = -1;
     if (from + lane < pg1) {
       const int v = from + lane;
-      entry = __ldg(bt + (v < sink_pages ? v : v + gap));
+      int col = v < front ? v : v + gap;
+      if (VIS == kSelected && v < front) {
+        col = __ldg(listed + v);
+        if (col >= front + gap) col = -1;  // not one of the list's candidates
+      }
+      if (VIS != kSelected || col >= 0) entry = __ldg(bt + col);
       if (entry < 0 || entry >= p.num_pages) {
         atomicOr(p.status, STATUS_BAD_PAGE);
         entry = -1;
@@ -237,12 +256,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     float sc[4];  // (row r, keys 2c, 2c + 1), (row r + 8, the same)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = ((acc[2][i] + acc[3][i]) + (acc[0][i] + acc[1][i])) * sl2;
-    const int v = u >> 1, key0 = (v < sink_pages ? v : v + gap) * kPageKeys + (u & 1) * kUnitKeys;
+    // (a listed page's place among the front pages stands for its column: its
+    // keys are all seen)
+    const int v = u >> 1, key0 = (v < front ? v : v + gap) * kPageKeys + (u & 1) * kUnitKeys;
     // all rows of the tile see all eight keys: up to the first row's position,
     // and sinks or inside the last row's window
     const int key1 = key0 + kUnitKeys - 1;
-    if (e < 0 || key1 > x0 || (key1 >= p.sinks && key0 <= x1 - p.window)) {
-      auto sees = [&](int x, int k) { return e >= 0 && k <= x && (k < p.sinks || k > x - p.window); };
+    if (e < 0 || key1 > x0 || (VIS == kWindow && key1 >= p.sinks && key0 <= x1 - p.window)) {
+      auto sees = [&](int x, int k) {
+        return e >= 0 && k <= x && (VIS == kSelected || k < p.sinks || k > x - p.window);
+      };
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = key0 + 2 * c + j;
@@ -391,12 +414,12 @@ constexpr int smem_bytes() {
 }
 
 // CTAs resident on an SM of the current device at a time (one tile per CTA).
-template <int D>
+template <int D, int VIS>
 int resident() {
   static PerDevice ctas;
   return std::max(1, ctas.get(current_device(), [] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false>, kWarps * 32,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false, VIS>, kWarps * 32,
                                                       smem_bytes<D, false>()) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -405,10 +428,10 @@ int resident() {
   }));
 }
 
-template <int D, bool ROWS>
+template <int D, bool ROWS, int VIS>
 cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, ROWS>();
-  const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D, ROWS>,
+  const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D, ROWS, VIS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int TM = (ROWS ? kWarps : 1) * kRows / (p.Hq / p.Hkv);
@@ -425,22 +448,23 @@ cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.fused ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, ROWS>, p);
+  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, ROWS, VIS>, p);
 }
 
-}  // namespace
-
-cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream) {
+template <int VIS>
+cudaError_t launch_seeing(const AttnParams &p, int sms, cudaStream_t stream) {
   const int G = p.Hq / p.Hkv;
   const int64_t tiles = (int64_t)p.Hkv * (((int64_t)p.num_tokens * G + kRows - 1) / kRows);
   if (p.num_tokens > p.num_seqs && tiles >= 8 * sms)  // two CTAs of four tiles on every SM
-    return p.D == 128 ? launch<128, true>(p, 1, stream) : launch<64, true>(p, 1, stream);
+    return p.D == 128 ? launch<128, true, VIS>(p, 1, stream) : launch<64, true, VIS>(p, 1, stream);
   // CTAs per tile: the number with the fewest rounds of resident CTAs, counted
   // in a warp's pages, a start and a join costing about three
   const int64_t pages = std::min<int64_t>(
-      p.max_pages, (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 2 + (p.sinks + kPageKeys - 1) / kPageKeys);
+      p.max_pages, VIS == kSelected ? (int64_t)p.budget + p.local_pages + kUnitRows / kPageKeys / G
+                                    : (int64_t)(p.window + kPageKeys - 1) / kPageKeys + 2 +
+                                          (p.sinks + kPageKeys - 1) / kPageKeys);
   const int64_t ctas = std::max<int64_t>(tiles, (int64_t)p.Hkv * p.num_seqs);
-  const int64_t slots = (int64_t)sms * (p.D == 128 ? resident<128>() : resident<64>());
+  const int64_t slots = (int64_t)sms * (p.D == 128 ? resident<128, VIS>() : resident<64, VIS>());
   int nc = 1;
   int64_t least = INT64_MAX;
   for (int n = 1; n <= 8; n *= 2) {
@@ -450,7 +474,14 @@ cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream)
       nc = n;
     }
   }
-  return p.D == 128 ? launch<128, false>(p, nc, stream) : launch<64, false>(p, nc, stream);
+  return p.D == 128 ? launch<128, false, VIS>(p, nc, stream) : launch<64, false, VIS>(p, nc, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream) {
+  return p.vis == kSelected ? launch_seeing<kSelected>(p, sms, stream)
+                            : launch_seeing<kWindow>(p, sms, stream);
 }
 
 }  // namespace cpa

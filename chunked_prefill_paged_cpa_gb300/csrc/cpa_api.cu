@@ -161,7 +161,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *query_start_loc,
               const int32_t *seq_lens, int32_t num_seqs, float scale, void *out,
               void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes,
-              const Window &win) {
+              const Sight &sight) {
   int rc = check_shape(desc);
   if (rc != CPA_OK) return rc;
   if (num_seqs < 0) return CPA_ERR_ARG;
@@ -205,13 +205,18 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.max_splits = w.max_splits;
   // positions stay below 2^30, and so do the window and the sinks: their sums
   // and differences stay in 32 bits
-  if (win.window && (int64_t)p.max_pages * p.page_size > (1 << 30)) return CPA_ERR_UNSUPPORTED;
-  p.window = std::min(win.window, 1 << 30);
-  p.sinks = std::min(win.sinks, 1 << 30);
+  const bool limited = sight.vis != kAll;
+  if (limited && (int64_t)p.max_pages * p.page_size > (1 << 30)) return CPA_ERR_UNSUPPORTED;
+  p.vis = sight.vis;
+  p.window = std::min(sight.window, 1 << 30);
+  p.sinks = std::min(sight.sinks, 1 << 30);
+  p.selected = sight.selected;
+  p.budget = sight.budget;
+  p.local_pages = std::min(sight.local_pages, 1 << 26);
   p.status = reinterpret_cast<uint32_t *>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   int grid = 0;
-  if (w.step || win.window) {
+  if (w.step || limited) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CPA_ERR_CUDA;
     grid = std::min(sm_count(dev), kMaxStepGrid);
@@ -227,12 +232,12 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     if (clear_bytes > desc->workspace_bytes) return CPA_ERR_WORKSPACE;
     if (cudaMemsetAsync(desc->workspace, 0, clear_bytes, st) != cudaSuccess) return CPA_ERR_CUDA;
   }
-  // with a window: fp32 steps, and steps of one token per sequence
-  const bool single = w.step && win.window && p.num_tokens == num_seqs && window_decode_takes(p, grid);
+  // with a window or selected pages: fp32 steps, and steps of one token per sequence
+  const bool single = w.step && limited && p.num_tokens == num_seqs && window_decode_takes(p, grid);
   // a mixed step's single tokens beside the step kernel of its chunks
-  const bool beside = w.step && win.window && p.num_tokens > num_seqs && num_seqs > 1 &&
+  const bool beside = w.step && limited && p.num_tokens > num_seqs && num_seqs > 1 &&
                       window_decode_beside(p, grid);
-  if (single || beside || (win.window && !w.step)) {
+  if (single || beside || (limited && !w.step)) {
     if (nr.k && launch_kv_append(nr.k, nr.v, nr.slots, const_cast<void *>(k_cache),
                                  const_cast<void *>(v_cache), desc->num_tokens, p.Hkv, p.D,
                                  p.page_size, p.num_pages, w.step ? 2 : 4,
@@ -267,9 +272,19 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     }
     if (w.q16) p.q16 = ws + w.q16;
     cudaError_t e;
-    if (p.kv_e4m3) e = win.window ? launch_step<2, true>(p, sw, st) : launch_step<2, false>(p, sw, st);
-    else if (p.act_f16) e = win.window ? launch_step<1, true>(p, sw, st) : launch_step<1, false>(p, sw, st);
-    else e = win.window ? launch_step<0, true>(p, sw, st) : launch_step<0, false>(p, sw, st);
+    const int mode = p.kv_e4m3 ? 2 : p.act_f16 ? 1 : 0;
+    if (p.vis == kAll)
+      e = mode == 2   ? launch_step<2, kAll>(p, sw, st)
+          : mode == 1 ? launch_step<1, kAll>(p, sw, st)
+                      : launch_step<0, kAll>(p, sw, st);
+    else if (p.vis == kWindow)
+      e = mode == 2   ? launch_step<2, kWindow>(p, sw, st)
+          : mode == 1 ? launch_step<1, kWindow>(p, sw, st)
+                      : launch_step<0, kWindow>(p, sw, st);
+    else
+      e = mode == 2   ? launch_step<2, kSelected>(p, sw, st)
+          : mode == 1 ? launch_step<1, kSelected>(p, sw, st)
+                      : launch_step<0, kSelected>(p, sw, st);
     if (e == cudaSuccess && beside) {
       p.rows_mode = 2;
       e = launch_window_decode(p, grid, st);
@@ -319,7 +334,22 @@ extern "C" int cpa_window_attention_forward(const void *q, const void *k_cache,
                                             void *out, void *stream, const cpa_desc *desc) {
   if (window < 1 || sinks < 0) return CPA_ERR_ARG;
   return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
-                   out, stream, desc, NewRows{}, 0, Window{window, sinks});
+                   out, stream, desc, NewRows{}, 0, Sight{kWindow, window, sinks});
+}
+
+extern "C" int cpa_selected_attention_forward(
+    const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+    const int32_t *query_start_loc, const int32_t *seq_lens, int32_t num_seqs, float scale,
+    const int32_t *selected, int32_t num_selected, int32_t local_pages, void *out, void *stream,
+    const cpa_desc *desc) {
+  if (num_selected < 0 || local_pages < 1) return CPA_ERR_ARG;
+  if (num_selected > kMaxSelected) return CPA_ERR_UNSUPPORTED;
+  if (num_selected > 0 && num_seqs > 0 && desc && desc->num_tokens > 0 &&
+      (!selected || !aligned(selected, 4)))
+    return CPA_ERR_ARG;
+  return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
+                   out, stream, desc, NewRows{}, 0,
+                   Sight{kSelected, 0, 0, selected, num_selected, local_pages});
 }
 
 // The append's arguments of the two fused calls; CPA_OK with no rows: nothing to do.
@@ -347,7 +377,7 @@ extern "C" int cpa_append_window_attention_forward(
   const int rc = append_args(k, v, slot_mapping, num_seqs, desc, &nr);
   if (rc != CPA_OK || !nr.k) return rc;
   return attention(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, num_seqs, scale,
-                   out, stream, desc, nr, 0, Window{window, sinks});
+                   out, stream, desc, nr, 0, Sight{kWindow, window, sinks});
 }
 
 extern "C" int cpa_append_attention_forward(const void *q, const void *k, const void *v,

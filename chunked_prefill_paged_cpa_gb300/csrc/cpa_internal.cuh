@@ -76,6 +76,13 @@ struct StepWs {
   int grid;            // CTAs of the step kernel (one per SM)
 };
 
+// Which keys the rows of an attention call see (include/cpa.h).
+enum Visible : int {
+  kAll = 0,       // every key up to the row's own
+  kWindow = 1,    // those in a window, and the sinks
+  kSelected = 2,  // those on selected pages, and on the last ones
+};
+
 struct AttnParams {
   const void *q;
   const void *k_cache;
@@ -91,9 +98,16 @@ struct AttnParams {
   int max_pages;
   float scale_log2;          // scale * log2(e): scores live in the log2 domain
   int max_splits;
-  // Sliding window (0: none): the row at position x sees key j <= x when
+  int vis;                    // Visible
+  // Sliding window (kWindow): the row at position x sees key j <= x when
   // j < sinks or j > x - window.
   int window, sinks;
+  // Selected pages (kSelected): the row at position x sees key j <= x on pages
+  // from L = unit_limit(x0) on, x0 the position of its unit's first token t0,
+  // and on the first min(budget, L) pages of the list selected[t0][kv head]
+  // (`budget` entries each).
+  const int32_t *selected;
+  int budget, local_pages;
   int rows_mode;              // row kernel, and windowed steps: 0 all tokens, 1 only q_len > 1,
                               // 2 only q_len == 1
   // Fused append (cpa_append_attention_forward, step kernel): the step's new
@@ -125,10 +139,30 @@ struct NewRows {
   const int64_t *slots = nullptr;
 };
 
-// Which keys a row sees (include/cpa.h); window 0: every key up to its own.
-struct Window {
-  int32_t window = 0, sinks = 0;
+// Which keys a row sees, as the entry points are told.
+struct Sight {
+  int32_t vis = kAll;
+  int32_t window = 0, sinks = 0;                                     // kWindow
+  const int32_t *selected = nullptr;                                 // kSelected
+  int32_t budget = 0, local_pages = 0;
 };
+
+// Tokens of a chunk that share a list of selected pages: a tile pair of the step
+// kernel.
+constexpr int kUnitRows = 256;
+// Entries of a list at most: the pages of 2^30 positions.
+constexpr int kMaxSelected = 1 << 26;
+
+// Bytes of a page's summary of one kv head: two codes per element, a scale, 12 zeros.
+constexpr int summary_row_bytes(int head_dim) { return 2 * head_dim + 16; }
+
+// Pages wholly before those that a unit whose first token is at position x sees
+// in any case: the candidates of its list.  (x div 16 + 1 at most 2^26.)
+__host__ __device__ __forceinline__ int unit_limit(int x, int local_pages) {
+  const int n = x / 16 + 1 - local_pages;
+  return n > 0 ? n : 0;
+}
+__device__ __forceinline__ int unit_limit(const AttnParams &p, int x) { return unit_limit(x, p.local_pages); }
 
 // The attention call behind every entry point (cpa_api.cu): validates the
 // arguments, optionally zeroes the first clear_bytes of the workspace on the
@@ -137,7 +171,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *query_start_loc,
               const int32_t *seq_lens, int32_t num_seqs, float scale, void *out,
               void *stream, const cpa_desc *desc, const NewRows &nr, size_t clear_bytes,
-              const Window &win = Window{});
+              const Sight &sight = Sight{});
 
 // Append of new rows; `quant` 0: copy elem_bytes-wide elements; 1 / 2: E4M3
 // codes of bf16 / binary16 rows divided by k_scale (K) and v_scale (V).
@@ -153,14 +187,16 @@ cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t s
 // (attn_chunk_tf32.cu); the decode rows then go to the row kernel (rows_mode 2).
 cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
 
-// A windowed step of single tokens with 16-bit queries (attn_window_decode.cu),
+// A step of single tokens with 16-bit queries that see a window or selected
+// pages (attn_window_decode.cu),
 // the new rows already in the cache; with rows_mode 2 the single tokens of a
 // mixed step, launched behind the step kernel of its chunks.
 bool window_decode_takes(const AttnParams &p, int sms);
 bool window_decode_beside(const AttnParams &p, int sms);
 cudaError_t launch_window_decode(const AttnParams &p, int sms, cudaStream_t stream);
 
-// A windowed fp32 step (attn_window_f32.cu), the new rows already in the cache.
+// A windowed fp32 step, or one over selected pages (attn_window_f32.cu), the new
+// rows already in the cache.
 cudaError_t launch_window_f32(const AttnParams &p, int sms, cudaStream_t stream);
 
 // Checks of the cache's shape shared by the calls (cpa_api.cu).
@@ -179,8 +215,8 @@ inline int current_device() {
 // 16-bit queries, head_dim 64/128, GQA group 1/2/4/8.  KVM 0: bf16 queries and
 // caches; 1: binary16 queries and caches; 2: E4M3 caches.
 bool step_path(int dtype, int D, int G);
-// WIN: with a sliding window (p.window >= 1).
-template <int KVM, bool WIN>
+// VIS: Visible.
+template <int KVM, int VIS>
 cudaError_t launch_step(const AttnParams &p, const StepWs &w, cudaStream_t stream);
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -69,7 +69,7 @@ int launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t sme
 // Copies.  The 16-byte words of all pairs' K and V pages are numbered through
 // (pair, then K or V, then the word within the page); a block takes 1024
 // consecutive words at a time, four per thread, all four loads before the
-// stores.
+// stores.  (The pages' summaries: one array, v_cache is null.)
 constexpr int kCopyThreads = 256, kCopyWords = 4;
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -79,7 +79,7 @@ copy_pages_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ d
   ptx::grid_dependency_wait();
   int n = max_pairs;
   if (num_pairs) n = min(max(ld32(num_pairs), 0), max_pairs);
-  const int pair_words = 2 * page_words;
+  const int pair_words = (v_cache ? 2 : 1) * page_words;
   const int64_t total = (int64_t)n * pair_words;
   constexpr int kStep = kCopyThreads * kCopyWords;
   for (int64_t base = (int64_t)blockIdx.x * kStep; base < total; base += (int64_t)gridDim.x * kStep) {
@@ -696,6 +696,30 @@ extern "C" size_t cpa_pages_workspace_bytes(int64_t num_pages) {
   return num_pages <= 0 || num_pages > INT32_MAX / kPageTokens ? 0 : pages_workspace(num_pages);
 }
 
+// Rows of `words` 16-byte words per page, in one array or (v not null) in two.
+static int copy_rows(const int32_t *src, const int32_t *dst, const int32_t *num_pairs,
+                     int32_t max_pairs, void *k, void *v, int64_t words, const cpa_desc *desc,
+                     void *stream) {
+  if (!src || !dst || !k || !aligned(src, 4) || !aligned(dst, 4) || !aligned(num_pairs, 4) ||
+      !aligned(k, 16) || !aligned(v, 16))
+    return CPA_ERR_ARG;
+  uint32_t *status = nullptr;
+  if (desc->workspace) {
+    if (!aligned(desc->workspace, 256) || desc->workspace_bytes < 256) return CPA_ERR_WORKSPACE;
+    status = static_cast<uint32_t *>(desc->workspace);
+  }
+  if (words > INT32_MAX / 4) return CPA_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CPA_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return CPA_ERR_CUDA;
+  const int64_t step = kCopyThreads * kCopyWords;
+  const int64_t blocks = ((int64_t)max_pairs * (v ? 2 : 1) * words + step - 1) / step;
+  return launch_chained(
+      copy_pages_kernel, dim3((unsigned)std::min<int64_t>(blocks, 16 * sms)), kCopyThreads, 0, (cudaStream_t)stream, 0, src, dst, num_pairs, max_pairs, static_cast<uint4 *>(k), static_cast<uint4 *>(v),
+      (int)words, desc->num_pages, status);
+}
+
 extern "C" int cpa_copy_pages(const int32_t *src, const int32_t *dst, const int32_t *num_pairs,
                               int32_t max_pairs, void *k_cache, void *v_cache,
                               const cpa_desc *desc, void *stream) {
@@ -703,26 +727,21 @@ extern "C" int cpa_copy_pages(const int32_t *src, const int32_t *dst, const int3
   if (rc != CPA_OK) return rc;
   if (max_pairs < 0) return CPA_ERR_ARG;
   if (max_pairs == 0) return CPA_OK;
-  if (!src || !dst || !k_cache || !v_cache || !aligned(src, 4) || !aligned(dst, 4) ||
-      !aligned(num_pairs, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
-    return CPA_ERR_ARG;
-  uint32_t *status = nullptr;
-  if (desc->workspace) {
-    if (!aligned(desc->workspace, 256) || desc->workspace_bytes < 256) return CPA_ERR_WORKSPACE;
-    status = static_cast<uint32_t *>(desc->workspace);
-  }
+  if (!v_cache) return CPA_ERR_ARG;
   const int eb = desc->kv_dtype == CPA_KV_E4M3 ? 1 : desc->dtype == CPA_F32 ? 4 : 2;
-  const int64_t words = (int64_t)desc->num_kv_heads * kPageTokens * desc->head_dim * eb / 16;
-  if (words > INT32_MAX / 4) return CPA_ERR_UNSUPPORTED;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return CPA_ERR_CUDA;
-  const int sms = sm_count(dev);
-  if (sms <= 0) return CPA_ERR_CUDA;
-  const int64_t step = kCopyThreads * kCopyWords;
-  const int64_t blocks = ((int64_t)max_pairs * 2 * words + step - 1) / step;
-  return launch_chained(
-      copy_pages_kernel, dim3((unsigned)std::min<int64_t>(blocks, 16 * sms)), kCopyThreads, 0, (cudaStream_t)stream, 0, src, dst, num_pairs, max_pairs, static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache),
-      (int)words, desc->num_pages, status);
+  return copy_rows(src, dst, num_pairs, max_pairs, k_cache, v_cache,
+                   (int64_t)desc->num_kv_heads * kPageTokens * desc->head_dim * eb / 16, desc, stream);
+}
+
+extern "C" int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *num_pairs,
+                                  int32_t max_pairs, void *summaries, const cpa_desc *desc,
+                                  void *stream) {
+  const int rc = check_shape(desc);
+  if (rc != CPA_OK) return rc;
+  if (max_pairs < 0) return CPA_ERR_ARG;
+  if (max_pairs == 0) return CPA_OK;
+  return copy_rows(src, dst, num_pairs, max_pairs, summaries, nullptr,
+                   (int64_t)desc->num_kv_heads * (summary_row_bytes(desc->head_dim) / 16), desc, stream);
 }
 
 extern "C" int cpa_fork_sequences(const int32_t *parents, const int32_t *children,

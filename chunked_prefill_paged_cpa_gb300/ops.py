@@ -98,6 +98,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.cpa_release_pages.restype = ctypes.c_int
         lib.cpa_compact_pages.argtypes = [P, I32, P, P, P, P, D, P]
         lib.cpa_compact_pages.restype = ctypes.c_int
+        lib.cpa_summary_bytes.argtypes = [D]
+        lib.cpa_summary_bytes.restype = Z
+        lib.cpa_summarise_pages.argtypes = [P, P, P, P, I32, P, D, P]
+        lib.cpa_summarise_pages.restype = ctypes.c_int
+        lib.cpa_copy_summaries.argtypes = [P, P, P, I32, P, D, P]
+        lib.cpa_copy_summaries.restype = ctypes.c_int
+        lib.cpa_select_pages.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P, P, D]
+        lib.cpa_select_pages.restype = ctypes.c_int
+        lib.cpa_selected_attention_forward.argtypes = [P, P, P, P, P, P, I32, F, P, I32, I32, P, P, D]
+        lib.cpa_selected_attention_forward.restype = ctypes.c_int
+        lib.cpa_pack_step.argtypes = [P, P, I32, P, P, I32, P, P, P, P, P, P, D, P]
+        lib.cpa_pack_step.restype = ctypes.c_int
         lib.cpa_attention_forward_noalloc.argtypes = [P, P, P, P, P, P, I32, F, P, P, D]
         lib.cpa_attention_forward_noalloc.restype = ctypes.c_int
         lib.cpa_read_device_status.argtypes = [D, P, ctypes.POINTER(I32)]
@@ -191,6 +203,44 @@ def cpa_compact_pages(block_table, num_rows, page_refs, copy_src, copy_dst, coun
                       desc: CpaDesc, stream) -> int:
     return int(load().cpa_compact_pages(block_table, int(num_rows), page_refs, copy_src, copy_dst,
                                         counts, ctypes.byref(desc), stream))
+
+
+def cpa_summary_bytes(desc: CpaDesc) -> int:
+    return int(load().cpa_summary_bytes(ctypes.byref(desc)))
+
+
+def cpa_summarise_pages(k_cache, block_table, query_start_loc, seq_lens, num_seqs, summaries,
+                        desc: CpaDesc, stream) -> int:
+    return int(load().cpa_summarise_pages(k_cache, block_table, query_start_loc, seq_lens,
+                                          int(num_seqs), summaries, ctypes.byref(desc), stream))
+
+
+def cpa_copy_summaries(src, dst, num_pairs, max_pairs, summaries, desc: CpaDesc, stream) -> int:
+    return int(load().cpa_copy_summaries(src, dst, num_pairs, int(max_pairs), summaries,
+                                         ctypes.byref(desc), stream))
+
+
+def cpa_select_pages(q, summaries, block_table, query_start_loc, seq_lens, num_seqs, num_selected,
+                     sink_pages, local_pages, selected, stream, desc: CpaDesc) -> int:
+    return int(load().cpa_select_pages(q, summaries, block_table, query_start_loc, seq_lens,
+                                       int(num_seqs), int(num_selected), int(sink_pages),
+                                       int(local_pages), selected, stream, ctypes.byref(desc)))
+
+
+def cpa_selected_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                                   num_seqs, scale, selected, num_selected, local_pages, out,
+                                   stream, desc: CpaDesc) -> int:
+    return int(load().cpa_selected_attention_forward(
+        q, k_cache, v_cache, block_table, query_start_loc, seq_lens, int(num_seqs), float(scale),
+        selected, int(num_selected), int(local_pages), out, stream, ctypes.byref(desc)))
+
+
+def cpa_pack_step(requests, new_tokens, num_requests, table, table_lens, num_rows, query_start_loc,
+                  seq_lens, block_table, positions, slot_mapping, counts, desc: CpaDesc,
+                  stream) -> int:
+    return int(load().cpa_pack_step(requests, new_tokens, int(num_requests), table, table_lens,
+                                    int(num_rows), query_start_loc, seq_lens, block_table,
+                                    positions, slot_mapping, counts, ctypes.byref(desc), stream))
 
 
 def cpa_attention_forward_noalloc(q, k_cache, v_cache, block_table, query_start_loc,
@@ -541,6 +591,121 @@ def compact_pages(block_table, page_refs, copy_src, copy_dst, counts, workspace,
     at = (table, rows, refs, *_pairs(copy_src, copy_dst, page_refs.shape[0] // 2, index),
           _expect("counts", counts, torch.int32, (2,), index))
     _launch("cpa_compact_pages", load().cpa_compact_pages, index, stream, at, desc, False)
+
+
+def summaries_for(k_cache: torch.Tensor) -> torch.Tensor:
+    """Zero-filled summaries of a cache's pages, uint8 [num_pages][Hkv][2 D + 16]."""
+    num_pages, hkv, _, d = k_cache.shape
+    if cpa_summary_bytes(make_desc(k_cache, hkv, 0, 1)) == 0:
+        raise CpaError(CPA_ERR_ARG, "cpa_summary_bytes")
+    return torch.zeros(num_pages, hkv, 2 * d + 16, dtype=torch.uint8, device=k_cache.device)
+
+
+def _metadata(block_table, query_start_loc, seq_lens, index: int) -> tuple:
+    """Checked (addresses of a batch's table, starts and lengths, sequences, columns)."""
+    table, (seqs, cols) = _expect_any("block_table", block_table, torch.int32, 2, index)
+    return (table, _expect("query_start_loc", query_start_loc, torch.int32, (seqs + 1,), index),
+            _expect("seq_lens", seq_lens, torch.int32, (seqs,), index)), seqs, cols
+
+
+def summarise_pages(k_cache, block_table, query_start_loc, seq_lens, summaries, workspace=None,
+                    stream=None) -> None:
+    """Summaries of the pages that the step's tokens complete, whose keys are in the cache."""
+    index, kdt = k_cache.get_device(), k_cache.dtype
+    kc, cache = _expect_any("k_cache", k_cache, kdt, 4, index)
+    where, seqs, cols = _metadata(block_table, query_start_loc, seq_lens, index)
+    at = _expect("summaries", summaries, torch.uint8, (cache[0], cache[1], 2 * cache[3] + 16), index)
+    desc = _cache_desc(k_cache, cache[1], 0, cols, workspace,
+                       torch.bfloat16 if kdt is torch.uint8 else kdt, 1.0, 1.0, index)
+    _launch("cpa_summarise_pages", load().cpa_summarise_pages, index, stream,
+            (kc, *where, seqs, at), desc, False)
+
+
+def _summary_desc(summaries, num_q_heads, num_tokens, cols, workspace, code, index):
+    """Checked address of summaries, and a descriptor of their cache's shape."""
+    at, (pages, hkv, row) = _expect_any("summaries", summaries, torch.uint8, 3, index)
+    ws = nb = 0
+    if workspace is not None:
+        ws, (nb,) = _expect_any("workspace", workspace, torch.uint8, 1, index)
+    if row not in (144, 272):
+        raise ValueError(f"summaries have rows of {row} bytes, expected 2 * head_dim + 16")
+    return at, CpaDesc(num_q_heads or hkv, hkv, (row - 16) // 2, 16, pages, cols, code, num_tokens,
+                       ws or None, nb, CPA_KV_SAME, 0.0, 0.0)
+
+
+def copy_summaries(src, dst, summaries, num_pairs=None, workspace=None, stream=None) -> None:
+    """Copies the summaries of pages ``src[i]`` to pages ``dst[i]``, of the lists of ``copy_pages``."""
+    index = summaries.get_device()
+    a, pairs = _expect_any("src", src, torch.int32, 1, index)
+    n = None
+    if num_pairs is not None:
+        n, (count,) = _expect_any("num_pairs", num_pairs, torch.int32, 1, index)
+        if count < 1:
+            raise ValueError("num_pairs is empty")
+    at, desc = _summary_desc(summaries, 0, 0, 1, workspace, CPA_BF16, index)
+    _launch("cpa_copy_summaries", load().cpa_copy_summaries, index, stream,
+            (a, _expect("dst", dst, torch.int32, pairs, index), n, pairs[0], at), desc, False)
+
+
+def select_pages(q, summaries, block_table, query_start_loc, seq_lens, selected, sink_pages=0,
+                 local_pages=1, workspace=None, stream=None) -> None:
+    """Fills ``selected`` (int32 [T][Hkv][n]): at the first token of every unit (a decode's token; of a
+    chunk runs of 256 / (Hq / Hkv) tokens) the n pages with the highest scores among the full ones before
+    the unit's last ``local_pages`` pages, in rising order, then -1."""
+    index = q.get_device()
+    code = _DTYPES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    qa, (tokens, heads, d) = _expect_any("q", q, q.dtype, 3, index)
+    where, seqs, cols = _metadata(block_table, query_start_loc, seq_lens, index)
+    at, desc = _summary_desc(summaries, heads, tokens, cols, workspace, code, index)
+    if d != desc.head_dim:
+        raise ValueError(f"q has head_dim {d}, the summaries have {desc.head_dim}")
+    to, shape = _expect_any("selected", selected, torch.int32, 3, index)
+    if shape[0] != tokens or shape[1] != desc.num_kv_heads:
+        raise ValueError(f"selected has shape {tuple(shape)}, expected ({tokens}, {desc.num_kv_heads}, n)")
+    _launch("cpa_select_pages", load().cpa_select_pages, index, stream,
+            (qa, at, *where, seqs, shape[2], _i32(sink_pages), _i32(local_pages), to), desc, True)
+
+
+def selected_attention_forward(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, scale,
+                               workspace, selected, local_pages=1, out=None, stream=None, k_scale=1.0,
+                               v_scale=1.0) -> torch.Tensor:
+    """Attention of the packed batch where a unit's rows see the pages listed for it in ``selected``
+    (int32 [T][Hkv][n], see ``select_pages``) and, causally, the pages from its last ``local_pages``
+    on.  Takes the workspace of ``workspace_for``."""
+    out, index, at, to, desc = _window_step(q, k_cache, v_cache, block_table, query_start_loc,
+                                            seq_lens, workspace, out, k_scale, v_scale)
+    pages, shape = _expect_any("selected", selected, torch.int32, 3, index)
+    if shape[0] != q.shape[0] or shape[1] != k_cache.shape[1]:
+        raise ValueError(f"selected has shape {tuple(shape)}, expected ({q.shape[0]}, {k_cache.shape[1]}, n)")
+    _launch("cpa_selected_attention_forward", load().cpa_selected_attention_forward, index, stream,
+            (*at, float(scale), pages, shape[2], _i32(local_pages), to), desc, True)
+    return out
+
+
+def pack_step(requests, new_tokens, table, table_lens, query_start_loc, seq_lens, block_table,
+              positions, slot_mapping, counts, num_pages=None, workspace=None, stream=None) -> None:
+    """A step's metadata: of the requests that take tokens (rows ``requests`` of ``table``; None: all rows in
+    order) the packed starts, lengths, page tables, positions and slots, and ``counts`` = (sequences, tokens).
+    ``table_lens`` counts the new tokens.  ``num_pages``: the pool's size, above which an entry is refused."""
+    index, i32 = table.get_device(), torch.int32
+    rows_at, (rows, cols) = _expect_any("table", table, i32, 2, index)
+    took, (n,) = _expect_any("new_tokens", new_tokens, i32, 1, index)
+    which = None if requests is None else _expect("requests", requests, i32, (n,), index)
+    slots, (tokens,) = _expect_any("slot_mapping", slot_mapping, torch.int64, 1, index)
+    ws = nb = 0
+    if workspace is not None:
+        ws, (nb,) = _expect_any("workspace", workspace, torch.uint8, 1, index)
+    at = (which, took, n, rows_at, _expect("table_lens", table_lens, i32, (rows,), index), rows,
+          _expect("query_start_loc", query_start_loc, i32, (n + 1,), index),
+          _expect("seq_lens", seq_lens, i32, (n,), index),
+          _expect("block_table", block_table, i32, (n, cols), index),
+          _expect("positions", positions, i32, (tokens,), index), slots,
+          _expect("counts", counts, i32, (2,), index))
+    pool = 2 ** 27 - 1 if num_pages is None else int(num_pages)
+    desc = CpaDesc(1, 1, 64, 16, pool, cols, CPA_BF16, tokens, ws or None, nb, CPA_KV_SAME, 0.0, 0.0)
+    _launch("cpa_pack_step", load().cpa_pack_step, index, stream, at, desc, False)
 
 
 def device_status(k_cache, num_q_heads, max_pages_per_seq, workspace, stream=None) -> int:

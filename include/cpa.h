@@ -70,8 +70,8 @@ typedef enum {
  * re-running.  Bit 4 alone means the GPU did not run the kernel's CTAs to
  * completion in time (for instance a stream starved for longer than the wait
  * limit by other work); the same call can simply be issued again.
- * The page operators also raise bit 8: a row that could not be forked,
- * extended or released (left as it was), and bit 16: cpa_extend_sequences
+ * The page operators and cpa_pack_step also raise bit 8: a row that could not be
+ * forked, extended, released (left as it was) or packed (left out), and bit 16: cpa_extend_sequences
  * found too few free pages (nothing was changed). */
 
 typedef enum { CPA_F32 = 0, CPA_BF16 = 1, CPA_F16 = 2 } cpa_dtype;
@@ -348,6 +348,120 @@ int cpa_release_pages(const int32_t *rows, int32_t num_released, int32_t *block_
 int cpa_compact_pages(int32_t *block_table, int32_t num_rows, int32_t *page_refs,
                       int32_t *copy_src, int32_t *copy_dst, int32_t *counts,
                       const cpa_desc *desc, void *stream);
+
+/* ---- Attention over selected pages ------------------------------------------
+ * Library extensions, for contexts of which each query should read a part only:
+ * every full page has a summary that bounds its keys, a cheap score made of it
+ * selects pages for each query, and the attention reads those and the last ones.
+ *
+ * A unit is the tokens that share a selection: the token of a sequence with
+ * q_len 1, and of a chunk runs of 256 / G tokens (G = num_q_heads / num_kv_heads)
+ * counted from its first token.  With x0 the position of the unit's first token,
+ *   L = max(0, x0 div 16 + 1 - local_pages)        (local_pages >= 1):
+ * the row at position x sees key j <= x when j div 16 >= L, or when page j div 16
+ * is one of the unit's min(num_selected, L) selected pages, which are pages
+ * 0 .. L - 1: full ones, written before the unit's first token.
+ *
+ * selected  int32 [num_tokens][num_kv_heads][num_selected]: the row of a unit's
+ *           first token holds its lists, as block-table columns; the rows of the
+ *           other tokens are neither read nor written.
+ * summaries [num_pages][num_kv_heads][2 * head_dim + 16] bytes, 16-byte aligned
+ *           (cpa_summary_bytes): int8 codes of the largest key element by element,
+ *           then of the smallest, the fp32 scale, 12 bytes of zeros.  They belong to
+ *           pages as the keys do: rows that share a page share its summary.
+ * At most 4096 sequences, max_pages_per_seq * 16 <= 2^30, num_pages < 2^27
+ * (CPA_ERR_UNSUPPORTED); without a status word (a workspace in desc) the calls
+ * other than the attention skip bad entries in silence. */
+
+/* Bytes of the summaries of desc->num_pages pages; 0 if the description is invalid. */
+size_t cpa_summary_bytes(const cpa_desc *desc);
+
+/* Summarises the pages that a step's tokens complete: columns
+ * (seq_lens[s] - q_len) div 16 .. seq_lens[s] div 16 - 1 of every sequence, whose
+ * keys are in the cache (cpa_kv_append, or an attention call with the append).  To
+ * make the summaries of whole sequences anew, describe them as chunks of all their
+ * tokens.  For keys K[t][d] of a page and kv head, in fp32 (an E4M3 cache: the
+ * codes' values, without the scale):
+ *   a = max |K|,  f = 127 / a,  scale = a / 127,
+ *   hi[d] = round(f * max_t K[t][d]),  lo[d] = round(f * min_t K[t][d]),
+ * each operation correctly rounded to fp32, round() to the nearest whole number,
+ * ties to even.  a < 2^-100: codes and scale are 0; a key that is not finite: the
+ * codes are 0, the scale is +infinity.  Sequences without tokens are left out; a
+ * table entry outside [0, num_pages) is skipped and raises the status word.
+ * Reads the cache's shape and type from desc, as cpa_kv_append does. */
+int cpa_summarise_pages(const void *k_cache, const int32_t *block_table,
+                        const int32_t *query_start_loc, const int32_t *seq_lens, int32_t num_seqs,
+                        void *summaries, const cpa_desc *desc, void *stream);
+
+/* The summaries of pages that move: as cpa_copy_pages, of the same lists. */
+int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *num_pairs,
+                       int32_t max_pairs, void *summaries, const cpa_desc *desc, void *stream);
+
+/* Selects pages for every unit and kv head: of the candidates 0 .. L - 1 the
+ * min(num_selected, L) with the highest scores, the lower page where scores are
+ * equal, listed in rising order; the list's other entries become -1.
+ * The score of a page is scale * (sum_d A[d] hi[d] + B[d] lo[d]), in whole numbers
+ * but for one fp32 product with the page's scale; it stands for the sum over the
+ * unit's rows (tokens by the G heads) of the largest logit that a key inside the
+ * bounds can have.  Of the unit's queries q[r][d], in fp32: a = max |q|,
+ * c = round(q * (127 / a)) as above (a < 2^-100, or a query that is not finite: 0),
+ * up[d] = sum_r max(c, 0), down[d] = sum_r max(-c, 0), h the least with
+ * max(up, down) div 2^h <= 127, A[d] = min(127, (up[d] + 2^h div 2) div 2^h) and
+ * -B[d] likewise of down[d].  Pages 0 .. sink_pages - 1 and pages whose scale is
+ * +infinity score +infinity; a page whose entry is outside [0, num_pages) comes
+ * behind all others and raises the status word.  Every candidate's summary must
+ * have been made.  A context of at most num_selected candidates reads none.
+ * sink_pages >= 0, num_selected >= 0 (0: nothing to do); max_pages_per_seq at most
+ * 393216 (CPA_ERR_UNSUPPORTED). */
+int cpa_select_pages(const void *q, const void *summaries, const int32_t *block_table,
+                     const int32_t *query_start_loc, const int32_t *seq_lens, int32_t num_seqs,
+                     int32_t num_selected, int32_t sink_pages, int32_t local_pages,
+                     int32_t *selected, void *stream, const cpa_desc *desc);
+
+/* Attention over the selected pages and the last ones.  The lists are those of
+ * cpa_select_pages, or any others: their first min(num_selected, L) entries are
+ * distinct columns of 0 .. L - 1, in any order; an entry outside is skipped and
+ * raises the status word.  num_selected may be 0 (selected is not read).
+ * Everything else is as in cpa_window_attention_forward: the whole packed batch,
+ * every dtype and cache storage, the workspace, the precision of fp32 steps; the
+ * cost is that of the keys that the units see.  Keys and values that no row of a
+ * unit sees may hold anything, NaN included. */
+int cpa_selected_attention_forward(const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_table, const int32_t *query_start_loc,
+                                   const int32_t *seq_lens, int32_t num_seqs, float scale,
+                                   const int32_t *selected, int32_t num_selected,
+                                   int32_t local_pages, void *out, void *stream,
+                                   const cpa_desc *desc);
+
+/* ---- Packing a step ----------------------------------------------------------
+ * The metadata of a step, on the device: request i takes new_tokens[i] tokens and
+ * is row requests[i] of `table` (int32 [num_rows][max_pages_per_seq]) and of
+ * table_lens (int32 [num_rows], its length with the new tokens counted, as
+ * cpa_extend_sequences takes it).  requests NULL: rows 0 .. num_requests - 1.
+ * Requests without tokens are left out, so the attention calls can take what comes
+ * out.  Of the n requests with tokens, in the list's order, T tokens in all:
+ *   query_start_loc int32 [num_requests + 1]: entries 0 .. n
+ *   seq_lens        int32 [num_requests]: entries 0 .. n - 1
+ *   block_table     int32 [num_requests][max_pages_per_seq]: of rows 0 .. n - 1 the
+ *                   columns that hold positions below seq_lens
+ *   positions       int32 [num_tokens], slot_mapping int64 [num_tokens]: entries
+ *                   0 .. T - 1, a token's position in its sequence and its slot (-1
+ *                   where the page's entry is outside [0, num_pages), which raises
+ *                   the status word)
+ *   counts          int32 [2]: n and T
+ * Nothing else is written.  The outputs are arrays of their own, apart from table.
+ * T > desc->num_tokens: nothing but counts = {0, -T} (at least -2^31 + 1) is
+ * written, and the status word is raised.  A request whose row is outside
+ * [0, num_rows), whose new_tokens is negative or above its length, or whose length
+ * is above max_pages_per_seq * 16, is left out and raises the status word (bit 8).
+ * Reads num_pages, page_size (16), max_pages_per_seq, num_tokens and, for the
+ * status word, workspace (may be NULL) from desc; at most 4096 requests
+ * (CPA_ERR_UNSUPPORTED). */
+int cpa_pack_step(const int32_t *requests, const int32_t *new_tokens, int32_t num_requests,
+                  const int32_t *table, const int32_t *table_lens, int32_t num_rows,
+                  int32_t *query_start_loc, int32_t *seq_lens, int32_t *block_table,
+                  int32_t *positions, int64_t *slot_mapping, int32_t *counts,
+                  const cpa_desc *desc, void *stream);
 
 /* Size of the scratch array built into the library for
  * cpa_attention_forward_noalloc: 64 MiB of device memory on every GPU that
