@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
 // ---------------------------------------------------------------------------
 // Selection.  A cluster of CTAs per (unit, kv head); each CTA scores a run of the
 // candidate pages and keeps the scores in its shared memory; the n-th largest is
-// found by its digits, eight bits at a time, over all of the cluster's scores.
-constexpr int kSelThreads = 128, kSelWarps = kSelThreads / 32;
+// found by its digits, eight bits at a time from the first that differs, over all
+// of the cluster's scores.
 constexpr int kDigits = 256;
+constexpr int kMaxCluster = 8;  // (portable)
 
 struct SelectArgs {
   const void *q;
@@ -222,8 +223,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 constexpr uint32_t kTopKey = 0xff800000u;  // of +infinity
 
-template <int QT, int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+template <int QT, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
+  constexpr int WARPS = THREADS / 32;
   constexpr int QB = QT == KEYS_F32 ? 4 : 2;
   constexpr int QN = 16 / QB;            // elements of 16 bytes of a query
   constexpr int ROW_BYTES = 2 * D + 16;  // of a summary
@@ -231,17 +233,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   extern __shared__ uint32_t keys[];     // [capacity]
   __shared__ int s_up[D], s_down[D];
   __shared__ __align__(16) int8_t s_codes[2 * D];
-  __shared__ int s_red[kSelWarps][2];
-  __shared__ int s_hist[kDigits];
-  __shared__ int s_more[2];  // this CTA's keys above the threshold, and at it
+  __shared__ int s_red[WARPS][3];
+  __shared__ __align__(16) int s_hist[4][kDigits], s_all[kDigits];
+  __shared__ uint32_t s_range[3];  // this CTA's ordinary keys: least, largest; its top keys
+  __shared__ int s_more[2];        // this CTA's keys above the threshold, and at it
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), g = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto sync = [&] { if (nc > 1) cluster.sync(); else __syncthreads(); };
 
   // The unit.  Number c < num_seqs is the first of sequence c; number num_seqs + m
-  // a later one whose first token is among TU m .. TU m + TU - 1: at most one is, and
-  // its sequence holds token TU m - 1.
+  // a later one whose first token is among TU w .. TU w + TU - 1, w = m + 1: at most
+  // one is, and its sequence holds token TU w - 1.
   const int TU = kUnitRows / a.G, c = blockIdx.x / nc;
   int s = c, first = 0;
   if (c >= a.num_seqs) {
@@ -267,16 +270,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   const int limit = unit_limit(max(0, ctx - q_len + first), a.local_pages);
   const int n = min(limit, a.budget);
   int32_t *list = a.selected + ((int64_t)t0 * a.Hkv + g) * a.budget;
-  for (int i = n + rank * kSelThreads + tid; i < a.budget; i += nc * kSelThreads) list[i] = -1;
+  for (int i = n + rank * THREADS + tid; i < a.budget; i += nc * THREADS) list[i] = -1;
   if (n == limit) {
-    for (int i = rank * kSelThreads + tid; i < n; i += nc * kSelThreads) list[i] = i;
+    for (int i = rank * THREADS + tid; i < n; i += nc * THREADS) list[i] = i;
     return;
   }
 
-  // The unit's rows as whole numbers: the largest magnitude, then the sums.
-  for (int i = tid; i < D; i += kSelThreads) s_up[i] = s_down[i] = 0;
+  // The unit's rows as whole numbers: the largest magnitude, then the sums.  A short
+  // last unit's last token counts for the tokens that it lacks.
+  for (int i = tid; i < D; i += THREADS) s_up[i] = s_down[i] = 0;
+  for (int i = tid; i < 4 * kDigits; i += THREADS) s_hist[0][i] = 0;
   constexpr int QL = D / QN;  // 16-byte words of a query
   const int words = tokens * a.G * QL;
+  const int last_weight = first > 0 ? 1 + TU - tokens : 1;
   auto load = [&](int w, float *f) {
     const int row = w / QL, tok = t0 + row / a.G, head = g * a.G + row % a.G;
     const uint4 x = __ldg(reinterpret_cast<const uint4 *>(
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   };
   float most = 0.f;
   bool fine = true;
-  for (int w = tid; w < words; w += kSelThreads) {
+  for (int w = tid; w < words; w += THREADS) {
     float f[QN];
     load(w, f);
 #pragma unroll
@@ -298,27 +304,28 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (lane == 0) s_red[warp][0] = __float_as_int(most);
   fine = __syncthreads_and(fine);
-  for (int w = 0; w < kSelWarps; ++w) most = fmaxf(most, __int_as_float(s_red[w][0]));
+  for (int w = 0; w < WARPS; ++w) most = fmaxf(most, __int_as_float(s_red[w][0]));
   const float factor = whole_factor(most, fine);
-  for (int w = tid; w < words; w += kSelThreads) {
+  for (int w = tid; w < words; w += THREADS) {
     float f[QN];
     load(w, f);
+    const int weight = w / (QL * a.G) == tokens - 1 ? last_weight : 1;
 #pragma unroll
     for (int e = 0; e < QN; ++e) {
       const int x = whole(f[e], factor);
-      if (x) atomicAdd((x > 0 ? s_up : s_down) + w % QL * QN + e, abs(x));
+      if (x) atomicAdd((x > 0 ? s_up : s_down) + w % QL * QN + e, weight * abs(x));
     }
   }
   __syncthreads();
   // seven bits of each sum, by the same shift
   int top = 0;
-  for (int i = tid; i < D; i += kSelThreads) top = max(top, max(s_up[i], s_down[i]));
+  for (int i = tid; i < D; i += THREADS) top = max(top, max(s_up[i], s_down[i]));
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) s_red[warp][1] = top;
   __syncthreads();
-  for (int w = 0; w < kSelWarps; ++w) top = max(top, s_red[w][1]);
+  for (int w = 0; w < WARPS; ++w) top = max(top, s_red[w][1]);
   const int shift = max(0, 25 - __clz(top)), half = (1 << shift) >> 1;
-  for (int i = tid; i < D; i += kSelThreads) {
+  for (int i = tid; i < D; i += THREADS) {
     s_codes[i] = (int8_t)min((s_up[i] + half) >> shift, 127);
     s_codes[D + i] = (int8_t)-min((s_down[i] + half) >> shift, 127);
   }
@@ -331,7 +338,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
 #pragma unroll
   for (int i = 0; i < CW; ++i) qc[i] = *reinterpret_cast<const int4 *>(s_codes + i * 64 + (lane & 3) * 16);
   const int32_t *bt = a.table + (int64_t)s * a.max_pages;
-  for (int j = j0 + warp * 32; j < j1; j += kSelThreads) {
+  uint32_t least = 0xffffffffu, largest = 0u;
+  int tops = 0;
+  for (int j = j0 + warp * 32; j < j1; j += THREADS) {
     int entry = -1;
     if (j + lane < j1) {
       entry = __ldg(bt + j + lane);
@@ -360,80 +369,143 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
       if ((lane & 3) == 0 && page < j1) {
         uint32_t key = scale < INFINITY ? order_key(__fmul_rn(scale, (float)sum)) : kTopKey;
         if (page < a.sink_pages) key = kTopKey;
-        keys[page - j0] = e < 0 ? 0u : key;
+        if (e < 0) key = 0u;
+        keys[page - j0] = key;
+        if (key == kTopKey) {
+          ++tops;
+        } else {
+          least = min(least, key);
+          largest = max(largest, key);
+        }
       }
     }
   }
+  least = __reduce_min_sync(0xffffffffu, least);
+  largest = __reduce_max_sync(0xffffffffu, largest);
+  tops = __reduce_add_sync(0xffffffffu, tops);
+  if (lane == 0) {
+    s_red[warp][0] = (int)least;
+    s_red[warp][1] = (int)largest;
+    s_red[warp][2] = tops;
+  }
+  __syncthreads();
+  tops = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    least = min(least, (uint32_t)s_red[w][0]);
+    largest = max(largest, (uint32_t)s_red[w][1]);
+    tops += s_red[w][2];
+  }
+  if (nc > 1) {
+    if (tid == 0) {
+      s_range[0] = least;
+      s_range[1] = largest;
+      s_range[2] = (uint32_t)tops;
+    }
+    cluster.sync();
+    tops = 0;
+    for (int b = 0; b < nc; ++b) {
+      const uint32_t *r = cluster.map_shared_rank(s_range, b);
+      least = min(least, r[0]);
+      largest = max(largest, r[1]);
+      tops += (int)r[2];
+    }
+  }
 
-  // The n-th largest key: digit by digit, the keys that share the digits found so
-  // far counted by the next one.
-  uint32_t found = 0, mask = 0;
-  int want = n;  // its place among those
-  for (int d = 24; d >= 0; d -= 8) {
-    for (int i = tid; i < kDigits; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < j1 - j0; i += kSelThreads) {
-      const uint32_t key = keys[i];
-      if ((key & mask) == found) atomicAdd(s_hist + (key >> d & 255u), 1);
-    }
-    sync();
-    // every warp of every CTA finds the digit for itself: a lane holds eight, from the top
-    int count[8], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      count[i] = 0;
-      for (int b = 0; b < nc; ++b)
-        count[i] += *(nc > 1 ? cluster.map_shared_rank(s_hist, b) + (255 - lane * 8 - i) : s_hist + (255 - lane * 8 - i));
-      sum += count[i];
-    }
-    int upto = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
-    int left = want - (upto - sum), digit = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (left > 0) {
-        digit = 255 - lane * 8 - i;
-        if (left <= count[i]) break;
-        left -= count[i];
+  // The n-th largest key: found under the mask, the `want` first of those that have
+  // its bits belong to the selection.  The digits from the highest bit in which the
+  // ordinary keys differ; until no key is left out of those with the bits found.
+  uint32_t found = kTopKey, mask = 0xffffffffu;
+  int want = n;
+  if (tops < n) {
+    want = n - tops;
+    int bits = 32 - __clz(least ^ largest);  // that differ
+    mask = bits == 32 ? 0u : 0xffffffffu << bits;
+    found = largest & mask;
+    for (int pass = 0; bits > 0; ++pass) {
+      const int d = max(0, bits - 8);
+      for (int i = tid; i < j1 - j0; i += THREADS) {
+        const uint32_t key = keys[i];
+        if (key != kTopKey && (key & mask) == found) atomicAdd(s_hist[pass] + ((key & ~mask) >> d), 1);
       }
+      sync();
+      const int *counts = s_hist[pass];
+      if (nc > 1) {
+        for (int i = tid; i < kDigits; i += THREADS) {
+          int x[kMaxCluster], sum = 0;
+#pragma unroll
+          for (int b = 0; b < kMaxCluster; ++b) x[b] = b < nc ? *cluster.map_shared_rank(s_hist[pass] + i, b) : 0;
+#pragma unroll
+          for (int b = 0; b < kMaxCluster; ++b) sum += x[b];
+          s_all[i] = sum;
+        }
+        __syncthreads();
+        counts = s_all;
+      }
+      // every warp finds the digit for itself: a lane holds eight, from the top
+      const int4 hi = *reinterpret_cast<const int4 *>(counts + 252 - lane * 8),
+                 lo = *reinterpret_cast<const int4 *>(counts + 248 - lane * 8);
+      const int count[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += count[i];
+      int upto = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
+      int left = want - (upto - sum), digit = 0, here = 0;
+      bool done = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!done) {
+          digit = 255 - lane * 8 - i;
+          here = count[i];
+          done = left <= here;
+          if (!done) left -= here;
+        }
+      }
+      digit = __shfl_sync(0xffffffffu, digit, owner);
+      here = __shfl_sync(0xffffffffu, here, owner);
+      want = __shfl_sync(0xffffffffu, left, owner);
+      found |= (uint32_t)digit << d;
+      mask = 0xffffffffu << d;
+      bits = d;
+      if (here == want) break;
+      if (nc > 1) __syncthreads();  // (s_all has been read)
     }
-    digit = __shfl_sync(0xffffffffu, digit, owner);
-    want = __shfl_sync(0xffffffffu, left, owner);
-    found |= (uint32_t)digit << d;
-    mask |= 255u << d;
-    sync();  // (the counts have been read)
   }
 
   // All keys above it, and the first `want` of those at it, in the pages' order.
   // A warp has a run of the pages.
-  const int run = ((j1 - j0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  auto at_it = [&](uint32_t key) { return (key & mask) == found && (key != kTopKey || found == kTopKey); };
+  const int run = ((j1 - j0 + WARPS - 1) / WARPS + 31) / 32 * 32;
   const int r0 = min(j1 - j0, warp * run), r1 = min(j1 - j0, r0 + run);
   int above = 0, at = 0;
   for (int i = r0 + lane; i < r1; i += 32) {
-    above += keys[i] > found;
-    at += keys[i] == found;
+    const uint32_t key = keys[i];
+    const bool eq = at_it(key);
+    above += !eq && key > found;
+    at += eq;
   }
   above = __reduce_add_sync(0xffffffffu, above);
   at = __reduce_add_sync(0xffffffffu, at);
+  __syncthreads();  // (s_red has been read)
   if (lane == 0) {
     s_red[warp][0] = above;
     s_red[warp][1] = at;
   }
   __syncthreads();
   above = at = 0;
-  for (int w = 0; w < kSelWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) {
       above += s_red[w][0];
       at += s_red[w][1];
     }
   }
   if (nc > 1) {
-    if (warp == kSelWarps - 1 && lane == 0) {
+    if (warp == WARPS - 1 && lane == 0) {
       s_more[0] = above + s_red[warp][0];
       s_more[1] = at + s_red[warp][1];
     }
@@ -446,7 +518,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   }
   for (int i = r0; i < r1; i += 32) {
     const uint32_t key = i + lane < r1 ? keys[i + lane] : 0u;
-    const bool gt = key > found, eq = i + lane < r1 && key == found;
+    const bool eq = i + lane < r1 && at_it(key), gt = i + lane < r1 && !eq && key > found;
     const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
     const unsigned low = (1u << lane) - 1u;
     const int eq_before = at + __popc(me & low);
@@ -488,10 +560,10 @@ cudaError_t launch_summarise(const SummariseArgs &a, int sms, cudaStream_t strea
 }
 
 // CTAs of a kernel resident on an SM with this much shared memory each.
-template <int QT, int D>
+template <int QT, int D, int THREADS>
 int select_resident(int smem) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, select_kernel<QT, D>, kSelThreads, smem) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, select_kernel<QT, D, THREADS>, THREADS, smem) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -499,18 +571,15 @@ int select_resident(int smem) {
 }
 
 constexpr int kMaxScores = 48 * 1024;  // of a CTA: 192 KB
-constexpr int kMaxCluster = 8;
 
-template <int QT, int D>
-cudaError_t launch_select(SelectArgs a, int sms, cudaStream_t stream) {
-  const int TU = kUnitRows / a.G;
-  const int64_t units = a.num_seqs + (a.num_tokens > a.num_seqs ? (a.num_tokens - 1) / TU : 0);
+template <int QT, int D, int THREADS>
+cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t stream) {
   const int device = current_device();
   static PerDevice configured;
   cudaError_t e = cudaSuccess;
   if (configured.get(device, [&] {
-        e = cudaFuncSetAttribute(select_kernel<QT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kMaxScores * 4);
+        e = cudaFuncSetAttribute(select_kernel<QT, D, THREADS>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxScores * 4);
         return e == cudaSuccess ? 1 : 0;
       }) < 1)
     return e;
@@ -521,8 +590,8 @@ cudaError_t launch_select(SelectArgs a, int sms, cudaStream_t stream) {
   for (int n = 1; n <= kMaxCluster; n *= 2) {
     const int per = (a.max_pages + n - 1) / n;
     if (per > kMaxScores) continue;
-    const int64_t slots = (int64_t)std::max(1, select_resident<QT, D>(per * 4)) * sms;
-    const int64_t cost = (units * a.Hkv * n + slots - 1) / slots * ((per + kSelThreads - 1) / kSelThreads + 10);
+    const int64_t slots = (int64_t)std::max(1, select_resident<QT, D, THREADS>(per * 4)) * sms;
+    const int64_t cost = (units * a.Hkv * n + slots - 1) / slots * ((per + THREADS - 1) / THREADS + 10);
     if (cost < least) {
       least = cost;
       nc = n;
@@ -531,7 +600,7 @@ cudaError_t launch_select(SelectArgs a, int sms, cudaStream_t stream) {
   a.capacity = (a.max_pages + nc - 1) / nc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * nc), a.Hkv);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = (size_t)a.capacity * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -540,7 +609,16 @@ cudaError_t launch_select(SelectArgs a, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<QT, D>, a);
+  return cudaLaunchKernelEx(&cfg, select_kernel<QT, D, THREADS>, a);
+}
+
+template <int QT, int D>
+cudaError_t launch_select(const SelectArgs &a, int sms, cudaStream_t stream) {
+  const int TU = kUnitRows / a.G;
+  const int64_t units = a.num_seqs + (a.num_tokens > a.num_seqs ? (a.num_tokens - 1) / TU : 0);
+  // units whose clusters leave SMs idle: as many loads on their way as an SM takes
+  return units * a.Hkv * kMaxCluster <= sms ? launch_select_on<QT, D, 512>(a, units, sms, stream)
+                                            : launch_select_on<QT, D, 128>(a, units, sms, stream);
 }
 
 }  // namespace

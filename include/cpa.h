@@ -405,7 +405,9 @@ int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *nu
  * unit's rows (tokens by the G heads) of the largest logit that a key inside the
  * bounds can have.  Of the unit's queries q[r][d], in fp32: a = max |q|,
  * c = round(q * (127 / a)) as above (a < 2^-100, or a query that is not finite: 0),
- * up[d] = sum_r max(c, 0), down[d] = sum_r max(-c, 0), h the least with
+ * up[d] = sum_r max(c, 0), down[d] = sum_r max(-c, 0) (every unit of a chunk of more
+ * than 256 / G tokens counts that many tokens: a short last one its last token once
+ * more for each that it lacks), h the least with
  * max(up, down) div 2^h <= 127, A[d] = min(127, (up[d] + 2^h div 2) div 2^h) and
  * -B[d] likewise of down[d].  Pages 0 .. sink_pages - 1 and pages whose scale is
  * +infinity score +infinity; a page whose entry is outside [0, num_pages) comes

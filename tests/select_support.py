@@ -99,7 +99,10 @@ def select(q, rows, table, q_lens, seq_lens, budget, sinks, local, selected):
         bad = (entries < 0) | (entries >= rows.shape[0])
         page = np.where(bad, 0, entries)
         for g in range(hkv):
-            whole = unit_codes(qn[t:t + n, g * group:(g + 1) * group].reshape(-1, d))
+            mine = qn[t:t + n, g * group:(g + 1) * group]
+            if x != seq_lens[s] - q_lens[s]:   # not the first unit: a short one's last token counts for those it lacks
+                mine = np.concatenate([mine, np.repeat(mine[-1:], 256 // group - n, 0)])
+            whole = unit_codes(mine.reshape(-1, d))
             with np.errstate(over="ignore", invalid="ignore"):
                 score = scales[page, g] * (codes[page, g] @ whole).astype(np.float32)
             score[~(scales[page, g] < np.inf)] = np.inf
