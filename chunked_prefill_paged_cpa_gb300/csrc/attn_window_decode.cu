@@ -505,6 +505,15 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t stream) {
     }
   }
   int nc = 1;
+  if constexpr (VIS == kSelected) {
+    // Lists are short beside a start and a join: as many CTAs as are resident at
+    // once, a page for each warp at least, one CTA where there are more rows.
+    // (bf16, 132 pages, 8 kv heads, tokens: 8 with 2 / 4 / 8 CTAs 20.6 / 17.0 / 22.9 us,
+    // 32 with 1 / 2 / 4 46 / 53 / 63, 128 with 1 / 2 / 4 179 / 189 / 214; 8-bit cache, 68
+    // pages: 8 with 4 / 8 9.5 / 9.1 us, 64 with 1 / 2 28 / 35.)
+    while (nc < kMaxCluster && rows * 2 * nc <= slots && 2 * nc * kWarps <= pages) nc *= 2;
+    return launch_on<KVM, D, kWarps, VIS>(p, nc, stream);
+  }
   int64_t least = INT64_MAX;
   for (int n = 1; n <= kMaxCluster; n *= 2) {
     const int64_t cost = (rows * n + slots - 1) / slots * ((pages + n * kWarps - 1) / (n * kWarps) + 3);

@@ -63,6 +63,25 @@ __device__ __forceinline__ void widen(const uint4 &x, float *f) {
   }
 }
 
+// The larger and the smaller of the elements of two words, NaN where either is:
+// fp32, or 16-bit pairs (E4M3 keys as binary16).
+template <int KT>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if constexpr (KT == KEYS_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else if constexpr (KT == KEYS_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <int KT>
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if constexpr (KT == KEYS_F32) asm("min.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else if constexpr (KT == KEYS_BF16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 // The scale and the factor to whole numbers of values whose largest magnitude is
 // `most`; fine: all of them are finite.
 __device__ __forceinline__ float whole_factor(float most, bool fine) {
@@ -120,52 +139,92 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
   __syncthreads();
 
   const int64_t items = (int64_t)sum * a.Hkv;
-  for (int64_t i = (int64_t)blockIdx.x * (kSumThreads / 32) + warp; i < items;
-       i += (int64_t)gridDim.x * (kSumThreads / 32)) {
-    const int n = (int)(i / a.Hkv), g = (int)(i - (int64_t)n * a.Hkv);
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] <= n) lo = mid; else hi = mid - 1;
-    }
-    int first;
-    pages_of(lo, first);
-    const int page = __ldg(a.table + (int64_t)lo * a.max_pages + first + n - before[lo]);
-    if (page < 0 || page >= a.num_pages) {
-      if (a.status && lane == 0) atomicOr(a.status, STATUS_BAD_PAGE);
-      continue;
-    }
-    const unsigned char *keys = a.k_cache + ((int64_t)page * a.Hkv + g) * (kPageTokens * D * EB) + lane * 16;
-    uint4 x[kPageTokens / ROWS];
-#pragma unroll
-    for (int r = 0; r < kPageTokens / ROWS; ++r) x[r] = __ldg(reinterpret_cast<const uint4 *>(keys + r * 512));
-    float up[N], down[N];
-    bool fine = true;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      up[e] = -INFINITY;
-      down[e] = INFINITY;
-    }
-#pragma unroll
-    for (int r = 0; r < kPageTokens / ROWS; ++r) {
-      float f[N];
-      widen<KT>(x[r], f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        fine &= fabsf(f[e]) < INFINITY;
-        up[e] = fmaxf(up[e], f[e]);
-        down[e] = fminf(down[e], f[e]);
+  const int64_t i0 = (int64_t)blockIdx.x * (kSumThreads / 32) + warp, stride = (int64_t)gridDim.x * (kSumThreads / 32);
+  // the warp's k-th item: its page and kv head's place in the caches, -1 for none;
+  // lane l looks up the l-th from the last look-up on
+  int64_t place = -1;
+  auto find = [&](int k) -> int64_t {
+    if ((k & 31) == 0) {
+      const int64_t i = i0 + (k + lane) * stride;
+      place = -1;
+      if (i < items) {
+        const int n = (int)(i / a.Hkv), g = (int)(i - (int64_t)n * a.Hkv);
+        int lo = 0, hi = S - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (before[mid] <= n) lo = mid; else hi = mid - 1;
+        }
+        int first;
+        pages_of(lo, first);
+        const int page = __ldg(a.table + (int64_t)lo * a.max_pages + first + n - before[lo]);
+        if (page >= 0 && page < a.num_pages) place = (int64_t)page * a.Hkv + g;
+        else if (a.status) atomicOr(a.status, STATUS_BAD_PAGE);
       }
     }
-    float most = 0.f;
+    return __shfl_sync(0xffffffffu, place, k & 31);
+  };
+  constexpr int LOADS = kPageTokens / ROWS;
+  auto load = [&](int64_t at, uint4 (&x)[LOADS]) {
+    const unsigned char *keys = a.k_cache + (at < 0 ? 0 : at) * (kPageTokens * D * EB) + lane * 16;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int r = 0; r < LOADS; ++r) x[r] = __ldg(reinterpret_cast<const uint4 *>(keys + r * 512));
+  };
+  if (i0 >= items) return;
+  const int count = (int)((items - i0 + stride - 1) / stride);
+  uint4 x[LOADS];
+  int64_t at = find(0);
+  load(at, x);
+  for (int k = 0; k < count; ++k) {
+    // (words of extremes: of E4M3 keys twice as many as were loaded)
+    constexpr int W = KT == KEYS_E4M3 ? 8 : 4;
+    uint32_t hi[W], lo[W];
+#pragma unroll
+    for (int r = 0; r < LOADS; ++r) {
+      uint32_t w[W];
+      if constexpr (KT == KEYS_E4M3) {
+        ptx::e4m3x4_to_f16x4(x[r].x, w[0], w[1]);
+        ptx::e4m3x4_to_f16x4(x[r].y, w[2], w[3]);
+        ptx::e4m3x4_to_f16x4(x[r].z, w[4], w[5]);
+        ptx::e4m3x4_to_f16x4(x[r].w, w[6], w[7]);
+      } else {
+        w[0] = x[r].x;
+        w[1] = x[r].y;
+        w[2] = x[r].z;
+        w[3] = x[r].w;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        hi[i] = r ? larger<KT>(hi[i], w[i]) : w[i];
+        lo[i] = r ? smaller<KT>(lo[i], w[i]) : w[i];
+      }
+    }
+    const int64_t now = at;
+    if (k + 1 < count) {
+      at = find(k + 1);
+      load(at, x);
+    }
+    if (now < 0) continue;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
 #pragma unroll
       for (int o = LANES; o < 32; o <<= 1) {
-        up[e] = fmaxf(up[e], __shfl_xor_sync(0xffffffffu, up[e], o));
-        down[e] = fminf(down[e], __shfl_xor_sync(0xffffffffu, down[e], o));
+        hi[i] = larger<KT>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        lo[i] = smaller<KT>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
       }
-      most = fmaxf(most, fmaxf(fabsf(up[e]), fabsf(down[e])));
+    }
+    float up[N], down[N], most = 0.f;
+    bool fine = true;
+    constexpr int WIDE = KT == KEYS_E4M3 ? KEYS_F16 : KT;
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      widen<WIDE>(make_uint4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]), up + i * (N / W));
+      widen<WIDE>(make_uint4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]), down + i * (N / W));
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float y = fmaxf(fabsf(up[e]), fabsf(down[e]));
+      fine &= fabsf(up[e]) < INFINITY && fabsf(down[e]) < INFINITY;
+      most = fmaxf(most, y);
     }
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -173,7 +232,7 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
     const float factor = whole_factor(most, fine);
     // the first group of lanes stores the largest, and the second (the same one,
     // where there is no second) the smallest
-    unsigned char *row = a.summaries + ((int64_t)page * a.Hkv + g) * ROW_BYTES;
+    unsigned char *row = a.summaries + now * ROW_BYTES;
     const int l = lane % LANES;
     auto store = [&](unsigned char *to, const float *f) {
       uint32_t w[N / 4];
@@ -201,6 +260,21 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
 // candidate pages and keeps the scores in its shared memory; the n-th largest is
 // found by its digits, eight bits at a time from the first that differs, over all
 // of the cluster's scores.
+//
+// What reads HBM at its rate is many warps with a whole turn of 32 summaries on its
+// way each, few instructions per summary, and CTAs enough on an SM that some read
+// while others search.  The turns go to shared memory by cp.async with consecutive
+// lanes on consecutive bytes, and are read a lane to a page.  (256 tokens of 8 kv
+// heads of 128, 256 to 1024 pages each, one CTA per list: 68 us, 5.2 TB/s; 1024
+// tokens of 640 pages 230 us, 6.2 TB/s.  With the words in registers, four lanes to
+// a page, 77 and 305 us; with the pages' places computed for every 16 bytes 79 us;
+// with two turns on their way, and so half the CTAs, 115 and 396 us; CTAs of 64, 96
+// and 256 threads 71, 67 and 88 us, and a hybrid step's selection, where a chunk's
+// units take longest, 40, 35 and 33 us against 28; clusters of two 102 us.)
+// A single unit waits for its chain: metadata, entries, summaries, then five or six
+// barriers of the cluster (6250 pages, 8 kv heads: 13.6 us; 63 us before every lane
+// fetched another CTA's counts).
+constexpr int kSelThreads = 128, kWideThreads = 256;
 constexpr int kDigits = 256;
 constexpr int kMaxCluster = 8;  // (portable)
 
@@ -229,23 +303,29 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   constexpr int QB = QT == KEYS_F32 ? 4 : 2;
   constexpr int QN = 16 / QB;            // elements of 16 bytes of a query
   constexpr int ROW_BYTES = 2 * D + 16;  // of a summary
-  constexpr int CW = 2 * D / 64;         // 16-byte words of a lane's part of it
-  extern __shared__ uint32_t keys[];     // [capacity]
-  __shared__ int s_up[D], s_down[D];
-  __shared__ __align__(16) int8_t s_codes[2 * D];
+  constexpr int CH = ROW_BYTES / 16;
+  // room for 32 summaries for every warp, then the keys [capacity]
+  extern __shared__ uint4 sm_select[];
+  uint32_t *keys = reinterpret_cast<uint32_t *>(sm_select + WARPS * 32 * CH);
+  __shared__ int s_sums[2 * D];
+  __shared__ __align__(16) int8_t s_codes[WARPS][2 * D];
   __shared__ int s_red[WARPS][3];
-  __shared__ __align__(16) int s_hist[4][kDigits], s_all[kDigits];
+  // (once the scores are there, in the rings' place)
+  int(*s_hist)[kDigits] = reinterpret_cast<int(*)[kDigits]>(sm_select), *s_all = s_hist[4];
   __shared__ uint32_t s_range[3];  // this CTA's ordinary keys: least, largest; its top keys
   __shared__ int s_more[2];        // this CTA's keys above the threshold, and at it
   cg::cluster_group cluster = cg::this_cluster();
-  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), g = blockIdx.y;
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  // the kv heads of a unit side by side: their rows of a page are neighbours in memory
+  const int number = blockIdx.x / nc, g = (gridDim.x / nc - 1 - number) % a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto sync = [&] { if (nc > 1) cluster.sync(); else __syncthreads(); };
 
   // The unit.  Number c < num_seqs is the first of sequence c; number num_seqs + m
   // a later one whose first token is among TU w .. TU w + TU - 1, w = m + 1: at most
   // one is, and its sequence holds token TU w - 1.
-  const int TU = kUnitRows / a.G, c = blockIdx.x / nc;
+  // (The last numbers first: units of chunks take longer.)
+  const int TU = kUnitRows / a.G, c = (gridDim.x / nc - 1 - number) / a.Hkv;
   int s = c, first = 0;
   if (c >= a.num_seqs) {
     const int64_t t = (int64_t)TU * (c - a.num_seqs + 1) - 1;
@@ -276,113 +356,192 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     return;
   }
 
-  // The unit's rows as whole numbers: the largest magnitude, then the sums.  A short
-  // last unit's last token counts for the tokens that it lacks.
-  for (int i = tid; i < D; i += THREADS) s_up[i] = s_down[i] = 0;
-  for (int i = tid; i < 4 * kDigits; i += THREADS) s_hist[0][i] = 0;
-  constexpr int QL = D / QN;  // 16-byte words of a query
-  const int words = tokens * a.G * QL;
-  const int last_weight = first > 0 ? 1 + TU - tokens : 1;
-  auto load = [&](int w, float *f) {
-    const int row = w / QL, tok = t0 + row / a.G, head = g * a.G + row % a.G;
+  // The CTA scores pages j0 .. j1 - 1, a warp 32 at a time; their entries are looked
+  // up one turn ahead.
+  const int per = (limit + nc - 1) / nc;  // (limit <= max_pages: at most the capacity)
+  const int j0 = min(limit, rank * per), j1 = min(limit, j0 + per);
+  const int32_t *bt = a.table + (int64_t)s * a.max_pages;
+  auto look_up = [&](int j) {
+    if (j + lane >= j1) return -1;
+    const int entry = __ldg(bt + j + lane);
+    if (entry >= 0 && entry < a.num_pages) return entry;
+    if (a.status) atomicOr(a.status, STATUS_BAD_PAGE);
+    return -1;
+  };
+  uint4 *ring = sm_select + warp * 32 * CH;
+  // 32 summaries on their way: the codes of 32 / CL of them at a time, consecutive
+  // lanes taking consecutive 16 bytes, then a scale for each lane
+  constexpr int CL = CH - 1;
+  auto fetch = [&](int entry) {
+    const unsigned char *from = a.summaries + (lane % CL) * 16;
+    uint4 *to = ring + lane / CL * CH + lane % CL;
+    const int mine = entry < 0 ? -1 : entry * a.Hkv + g;  // (at most num_pages Hkv - 1, see the host's checks)
+#pragma unroll
+    for (int i = 0; i < CL; ++i) {
+      const int row = __shfl_sync(0xffffffffu, mine, i * (32 / CL) + lane / CL);
+      ptx::cp_async16(to + i * (32 / CL) * CH, from + (int64_t)max(row, 0) * ROW_BYTES, row < 0 ? 0 : 16);
+    }
+    ptx::cp_async16(ring + lane * CH + CL, a.summaries + (int64_t)max(mine, 0) * ROW_BYTES + 2 * D, mine < 0 ? 0 : 16);
+    ptx::cp_async_commit();
+  };
+  int entry = look_up(j0 + warp * 32), next = look_up(j0 + warp * 32 + THREADS);
+  fetch(entry);
+
+  // The unit's rows as whole numbers: the largest magnitude, then the sums, then
+  // seven bits of each by the same shift.  A short last unit's last token counts for
+  // the tokens that it lacks.
+  constexpr int QL = D / QN;  // 16-byte words of a query; a lane's stand at the same dims
+  static_assert(QL <= 32, "a row fits a warp");
+  const int rows = tokens * a.G, last_weight = first > 0 ? 1 + TU - tokens : 1;
+  auto load = [&](int row, float *f) {
+    const int tok = t0 + row / a.G, head = g * a.G + row % a.G;
     const uint4 x = __ldg(reinterpret_cast<const uint4 *>(
-        static_cast<const unsigned char *>(a.q) + (((int64_t)tok * a.Hkv * a.G + head) * D) * QB) + w % QL);
+        static_cast<const unsigned char *>(a.q) + (((int64_t)tok * a.Hkv * a.G + head) * D) * QB) + lane % QL);
     widen<QT>(x, f);
   };
-  float most = 0.f;
-  bool fine = true;
-  for (int w = tid; w < words; w += THREADS) {
-    float f[QN];
-    load(w, f);
+  int up[QN] = {}, down[QN] = {};
+  auto add = [&](const float *f, float factor, int weight) {
 #pragma unroll
     for (int e = 0; e < QN; ++e) {
-      fine &= fabsf(f[e]) < INFINITY;
-      most = fmaxf(most, fabsf(f[e]));
+      const int x = weight * whole(f[e], factor);
+      up[e] += max(x, 0);
+      down[e] += max(-x, 0);
     }
-  }
+  };
+  auto join_lanes = [&] {  // those of a warp at the same dims
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) s_red[warp][0] = __float_as_int(most);
-  fine = __syncthreads_and(fine);
-  for (int w = 0; w < WARPS; ++w) most = fmaxf(most, __int_as_float(s_red[w][0]));
-  const float factor = whole_factor(most, fine);
-  for (int w = tid; w < words; w += THREADS) {
-    float f[QN];
-    load(w, f);
-    const int weight = w / (QL * a.G) == tokens - 1 ? last_weight : 1;
+    for (int e = 0; e < QN; ++e)
+#pragma unroll
+      for (int o = QL; o < 32; o <<= 1) {
+        up[e] += __shfl_xor_sync(0xffffffffu, up[e], o);
+        down[e] += __shfl_xor_sync(0xffffffffu, down[e], o);
+      }
+  };
+  int8_t *codes = s_codes[warp];
+  if (tokens == 1) {
+    // a single token: every warp for itself, nothing to wait for
+    constexpr int MOST = 8 * QL / 32;  // rows of a lane: 8 heads at most
+    float f[MOST][QN], most = 0.f;
+    bool fine = true;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const int row = i * (32 / QL) + lane / QL;
+#pragma unroll
+      for (int e = 0; e < QN; ++e) f[i][e] = 0.f;
+      if (row < rows) load(row, f[i]);
+#pragma unroll
+      for (int e = 0; e < QN; ++e) {
+        fine &= fabsf(f[i][e]) < INFINITY;
+        most = fmaxf(most, fabsf(f[i][e]));
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float factor = whole_factor(most, __all_sync(0xffffffffu, fine));
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) add(f[i], factor, last_weight);
+    join_lanes();
+  } else {
+    constexpr int STEP = THREADS / QL;  // rows of the CTA at a time
+    const int row0 = warp * (32 / QL) + lane / QL;
+    float most = 0.f;
+    bool fine = true;
+#pragma unroll 4
+    for (int row = row0; row < rows; row += STEP) {
+      float f[QN];
+      load(row, f);
+#pragma unroll
+      for (int e = 0; e < QN; ++e) {
+        fine &= fabsf(f[e]) < INFINITY;
+        most = fmaxf(most, fabsf(f[e]));
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) s_red[warp][0] = __float_as_int(most);
+    for (int i = tid; i < 2 * D; i += THREADS) s_sums[i] = 0;
+    fine = __syncthreads_and(fine);
+    for (int w = 0; w < WARPS; ++w) most = fmaxf(most, __int_as_float(s_red[w][0]));
+    const float factor = whole_factor(most, fine);
+#pragma unroll 4
+    for (int row = row0; row < rows; row += STEP) {
+      float f[QN];
+      load(row, f);
+      add(f, factor, row / a.G == tokens - 1 ? last_weight : 1);
+    }
+    join_lanes();
+    if (lane < QL) {
+#pragma unroll
+      for (int e = 0; e < QN; ++e) {
+        atomicAdd(s_sums + lane * QN + e, up[e]);
+        atomicAdd(s_sums + D + lane * QN + e, down[e]);
+      }
+    }
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < QN; ++e) {
-      const int x = whole(f[e], factor);
-      if (x) atomicAdd((x > 0 ? s_up : s_down) + w % QL * QN + e, weight * abs(x));
+      up[e] = s_sums[lane % QL * QN + e];
+      down[e] = s_sums[D + lane % QL * QN + e];
     }
   }
-  __syncthreads();
-  // seven bits of each sum, by the same shift
-  int top = 0;
-  for (int i = tid; i < D; i += THREADS) top = max(top, max(s_up[i], s_down[i]));
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_red[warp][1] = top;
-  __syncthreads();
-  for (int w = 0; w < WARPS; ++w) top = max(top, s_red[w][1]);
-  const int shift = max(0, 25 - __clz(top)), half = (1 << shift) >> 1;
-  for (int i = tid; i < D; i += THREADS) {
-    s_codes[i] = (int8_t)min((s_up[i] + half) >> shift, 127);
-    s_codes[D + i] = (int8_t)-min((s_down[i] + half) >> shift, 127);
+  {
+    int top = 0;
+#pragma unroll
+    for (int e = 0; e < QN; ++e) top = max(top, max(up[e], down[e]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int shift = max(0, 25 - __clz(top)), half = (1 << shift) >> 1;
+    if (lane < QL) {
+#pragma unroll
+      for (int e = 0; e < QN; ++e) {
+        codes[lane * QN + e] = (int8_t)min((up[e] + half) >> shift, 127);
+        codes[D + lane * QN + e] = (int8_t)-min((down[e] + half) >> shift, 127);
+      }
+    }
+    __syncwarp();
   }
-  __syncthreads();
 
-  // Scores of pages j0 .. j1 - 1: four lanes to a page, a warp 32 pages at a time.
-  const int per = (limit + nc - 1) / nc;
-  const int j0 = min(limit, rank * per), j1 = min(limit, j0 + per);
-  int4 qc[CW];
-#pragma unroll
-  for (int i = 0; i < CW; ++i) qc[i] = *reinterpret_cast<const int4 *>(s_codes + i * 64 + (lane & 3) * 16);
-  const int32_t *bt = a.table + (int64_t)s * a.max_pages;
+  // The scores, a lane to a page (its 16-byte words 4 banks from the next lane's).
   uint32_t least = 0xffffffffu, largest = 0u;
   int tops = 0;
   for (int j = j0 + warp * 32; j < j1; j += THREADS) {
-    int entry = -1;
-    if (j + lane < j1) {
-      entry = __ldg(bt + j + lane);
-      if (entry < 0 || entry >= a.num_pages) {
-        if (a.status) atomicOr(a.status, STATUS_BAD_PAGE);
-        entry = -1;
+    ptx::cp_async_wait<0>();
+    __syncwarp();
+    const uint4 *row = ring + lane * CH;
+    int sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < CH - 1; ++i) {
+      const uint4 x = row[i], q = reinterpret_cast<const uint4 *>(codes)[i];
+      sum[0] = __dp4a((int)x.x, (int)q.x, sum[0]);
+      sum[1] = __dp4a((int)x.y, (int)q.y, sum[1]);
+      sum[0] = __dp4a((int)x.z, (int)q.z, sum[0]);
+      sum[1] = __dp4a((int)x.w, (int)q.w, sum[1]);
+    }
+    const float scale = __uint_as_float(row[CH - 1].x);
+    const int page = j + lane;
+    if (page < j1) {
+      uint32_t key = scale < INFINITY ? order_key(__fmul_rn(scale, (float)(sum[0] + sum[1]))) : kTopKey;
+      if (page < a.sink_pages) key = kTopKey;
+      if (entry < 0) key = 0u;
+      keys[page - j0] = key;
+      if (key == kTopKey) {
+        ++tops;
+      } else {
+        least = min(least, key);
+        largest = max(largest, key);
       }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = __shfl_sync(0xffffffffu, entry, k * 8 + (lane >> 2));
-      const unsigned char *row = a.summaries + ((int64_t)max(e, 0) * a.Hkv + g) * ROW_BYTES;
-      int sum = 0;
-#pragma unroll
-      for (int i = 0; i < CW; ++i) {
-        const int4 x = __ldg(reinterpret_cast<const int4 *>(row + i * 64 + (lane & 3) * 16));
-        sum = __dp4a(x.x, qc[i].x, sum);
-        sum = __dp4a(x.y, qc[i].y, sum);
-        sum = __dp4a(x.z, qc[i].z, sum);
-        sum = __dp4a(x.w, qc[i].w, sum);
-      }
-      const float scale = __ldg(reinterpret_cast<const float *>(row + 2 * D));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int page = j + k * 8 + (lane >> 2);
-      if ((lane & 3) == 0 && page < j1) {
-        uint32_t key = scale < INFINITY ? order_key(__fmul_rn(scale, (float)sum)) : kTopKey;
-        if (page < a.sink_pages) key = kTopKey;
-        if (e < 0) key = 0u;
-        keys[page - j0] = key;
-        if (key == kTopKey) {
-          ++tops;
-        } else {
-          least = min(least, key);
-          largest = max(largest, key);
-        }
-      }
+    __syncwarp();
+    entry = next;
+    if (j + THREADS < j1) {
+      fetch(entry);
+      next = look_up(j + 2 * THREADS);
     }
   }
   least = __reduce_min_sync(0xffffffffu, least);
   largest = __reduce_max_sync(0xffffffffu, largest);
   tops = __reduce_add_sync(0xffffffffu, tops);
+  __syncthreads();  // (s_red and the rings have been read)
+  for (int i = tid; i < 4 * kDigits; i += THREADS) s_hist[0][i] = 0;
   if (lane == 0) {
     s_red[warp][0] = (int)least;
     s_red[warp][1] = (int)largest;
@@ -402,13 +561,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
       s_range[2] = (uint32_t)tops;
     }
     cluster.sync();
-    tops = 0;
-    for (int b = 0; b < nc; ++b) {
-      const uint32_t *r = cluster.map_shared_rank(s_range, b);
-      least = min(least, r[0]);
-      largest = max(largest, r[1]);
-      tops += (int)r[2];
-    }
+    // (a lane to a CTA: one round trip)
+    const uint32_t *r = cluster.map_shared_rank(s_range, min(lane, nc - 1));
+    least = __reduce_min_sync(0xffffffffu, r[0]);
+    largest = __reduce_max_sync(0xffffffffu, r[1]);
+    tops = __reduce_add_sync(0xffffffffu, lane < nc ? (int)r[2] : 0);
   }
 
   // The n-th largest key: found under the mask, the `want` first of those that have
@@ -510,10 +667,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
       s_more[1] = at + s_red[warp][1];
     }
     cluster.sync();
-    for (int b = 0; b < rank; ++b) {
-      above += *cluster.map_shared_rank(s_more, b);
-      at += *cluster.map_shared_rank(s_more + 1, b);
-    }
+    const int *more = cluster.map_shared_rank(s_more, min(lane, nc - 1));
+    above += __reduce_add_sync(0xffffffffu, lane < rank ? more[0] : 0);
+    at += __reduce_add_sync(0xffffffffu, lane < rank ? more[1] : 0);
     cluster.sync();  // no CTA leaves while another reads its counts
   }
   for (int i = r0; i < r1; i += 32) {
@@ -555,7 +711,17 @@ template <int KT, int D>
 cudaError_t launch_summarise(const SummariseArgs &a, int sms, cudaStream_t stream) {
   // (48 KB of shared memory at most: 4097 words)
   const size_t smem = sizeof(int) * ((size_t)a.num_seqs + 1);
-  summarise_kernel<KT, D><<<4 * sms, kSumThreads, smem, stream>>>(a);
+  // as many CTAs as are resident at once
+  static PerDevice ctas;
+  const int resident = std::max(1, ctas.get(current_device(), [] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, summarise_kernel<KT, D>, kSumThreads, 0) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return n;
+  }));
+  summarise_kernel<KT, D><<<resident * sms, kSumThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -570,16 +736,19 @@ int select_resident(int smem) {
   return n;
 }
 
-constexpr int kMaxScores = 48 * 1024;  // of a CTA: 192 KB
+constexpr int kMaxScores = 32 * 1024;  // of a CTA: 128 KB
+constexpr int kSharedLimit = 216 * 1024;  // beside the static part
 
 template <int QT, int D, int THREADS>
 cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t stream) {
+  constexpr int ring = THREADS * (2 * D + 16);
+  static_assert(ring >= 5 * kDigits * 4, "the counts fit the rings");
   const int device = current_device();
   static PerDevice configured;
   cudaError_t e = cudaSuccess;
   if (configured.get(device, [&] {
         e = cudaFuncSetAttribute(select_kernel<QT, D, THREADS>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxScores * 4);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedLimit);
         return e == cudaSuccess ? 1 : 0;
       }) < 1)
     return e;
@@ -589,8 +758,8 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
   int64_t least = INT64_MAX;
   for (int n = 1; n <= kMaxCluster; n *= 2) {
     const int per = (a.max_pages + n - 1) / n;
-    if (per > kMaxScores) continue;
-    const int64_t slots = (int64_t)std::max(1, select_resident<QT, D, THREADS>(per * 4)) * sms;
+    if (per > kMaxScores || ring + per * 4 > kSharedLimit) continue;
+    const int64_t slots = (int64_t)std::max(1, select_resident<QT, D, THREADS>(ring + per * 4)) * sms;
     const int64_t cost = (units * a.Hkv * n + slots - 1) / slots * ((per + THREADS - 1) / THREADS + 10);
     if (cost < least) {
       least = cost;
@@ -599,9 +768,9 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
   }
   a.capacity = (a.max_pages + nc - 1) / nc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * nc), a.Hkv);
+  cfg.gridDim = dim3((unsigned)(units * a.Hkv * nc));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)a.capacity * 4;
+  cfg.dynamicSmemBytes = ring + (size_t)a.capacity * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -617,8 +786,10 @@ cudaError_t launch_select(const SelectArgs &a, int sms, cudaStream_t stream) {
   const int TU = kUnitRows / a.G;
   const int64_t units = a.num_seqs + (a.num_tokens > a.num_seqs ? (a.num_tokens - 1) / TU : 0);
   // units whose clusters leave SMs idle: as many loads on their way as an SM takes
-  return units * a.Hkv * kMaxCluster <= sms ? launch_select_on<QT, D, 512>(a, units, sms, stream)
-                                            : launch_select_on<QT, D, 128>(a, units, sms, stream);
+  const bool few = units * a.Hkv * kMaxCluster <= sms &&
+                   kWideThreads * (2 * D + 16) + (a.max_pages + kMaxCluster - 1) / kMaxCluster * 4 <= kSharedLimit;
+  return few ? launch_select_on<QT, D, kWideThreads>(a, units, sms, stream)
+             : launch_select_on<QT, D, kSelThreads>(a, units, sms, stream);
 }
 
 }  // namespace
@@ -682,7 +853,8 @@ extern "C" int cpa_select_pages(const void *q, const void *summaries, const int3
   if (!q || !summaries || !selected || !aligned(q, 16) || !aligned(summaries, 16) || !aligned(selected, 4))
     return CPA_ERR_ARG;
   if ((rc = check_batch(desc, num_seqs, block_table, query_start_loc, seq_lens)) != CPA_OK) return rc;
-  if (desc->max_pages_per_seq > kMaxCluster * kMaxScores) return CPA_ERR_UNSUPPORTED;
+  if (desc->max_pages_per_seq > kMaxCluster * kMaxScores || desc->num_pages * desc->num_kv_heads > INT32_MAX)
+    return CPA_ERR_UNSUPPORTED;
   SelectArgs a{};
   if ((rc = status_of(desc, &a.status)) != CPA_OK) return rc;
   a.q = q;

@@ -414,7 +414,7 @@ int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *nu
  * behind all others and raises the status word.  Every candidate's summary must
  * have been made.  A context of at most num_selected candidates reads none.
  * sink_pages >= 0, num_selected >= 0 (0: nothing to do); max_pages_per_seq at most
- * 393216 (CPA_ERR_UNSUPPORTED). */
+ * 262144 (CPA_ERR_UNSUPPORTED). */
 int cpa_select_pages(const void *q, const void *summaries, const int32_t *block_table,
                      const int32_t *query_start_loc, const int32_t *seq_lens, int32_t num_seqs,
                      int32_t num_selected, int32_t sink_pages, int32_t local_pages,

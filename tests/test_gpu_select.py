@@ -166,7 +166,7 @@ def test_scores_past_the_largest_number(cuda_device):
         run_select(q, rows, where, table, [1], [200 * 16], budget, 0, 1, cuda_device)
 
 
-@pytest.mark.parametrize("length,columns", [(100003, None), (500, 20000), (30000, 300000)])
+@pytest.mark.parametrize("length,columns", [(100003, None), (500, 20000), (30000, 260000)])
 def test_long_contexts_and_wide_tables(cuda_device, length, columns):
     """Candidates over the CTAs of a cluster; columns that no context reaches."""
     pages = -(-length // PAGE) + 1

@@ -66,7 +66,7 @@ def test_selection_refuses():
         assert choose(**{name: None}) == ops.CPA_ERR_ARG, name
     assert choose(sum=OFF8) == choose(q=OFF8) == choose(sel=ODD) == choose(bt=ODD) == ops.CPA_ERR_ARG
     assert choose(desc(max_pages_per_seq=0)) == ops.CPA_ERR_ARG
-    assert choose(desc(max_pages_per_seq=393217)) == choose(desc(num_pages=1 << 27)) == choose(desc(page_size=32)) == ops.CPA_ERR_UNSUPPORTED
+    assert choose(desc(max_pages_per_seq=262145)) == choose(desc(num_pages=1 << 27)) == choose(desc(page_size=32)) == ops.CPA_ERR_UNSUPPORTED
     assert choose(desc(num_tokens=5000), n=4097) == ops.CPA_ERR_UNSUPPORTED
     assert choose(desc(workspace=4100, workspace_bytes=256)) == choose(desc(workspace=4096, workspace_bytes=64)) == ops.CPA_ERR_WORKSPACE
     assert choose(pages=0, sel=None) == choose(desc(num_tokens=0)) == choose(n=0) == ops.CPA_OK
