@@ -725,15 +725,22 @@ cudaError_t launch_summarise(const SummariseArgs &a, int sms, cudaStream_t strea
   return cudaGetLastError();
 }
 
-// CTAs of a kernel resident on an SM with this much shared memory each.
+// CTAs of the selection's kernel resident on an SM of the current device, each with
+// this much shared memory of its own choice: what registers and the kernel's own
+// shared memory allow, found once, and what the shared memory does.
 template <int QT, int D, int THREADS>
-int select_resident(int smem) {
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, select_kernel<QT, D, THREADS>, THREADS, smem) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  return n;
+int64_t select_resident(int smem) {
+  constexpr int kSm = 228 * 1024, kOwn = 5 * 1024;  // an SM's; a CTA's static part and the system's 1 KB
+  static PerDevice ctas;
+  const int most = std::max(1, ctas.get(current_device(), [] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, select_kernel<QT, D, THREADS>, THREADS, 0) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return n;
+  }));
+  return std::max(1, std::min(most, kSm / (smem + kOwn)));
 }
 
 constexpr int kMaxScores = 32 * 1024;  // of a CTA: 128 KB
@@ -759,7 +766,7 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
   for (int n = 1; n <= kMaxCluster; n *= 2) {
     const int per = (a.max_pages + n - 1) / n;
     if (per > kMaxScores || ring + per * 4 > kSharedLimit) continue;
-    const int64_t slots = (int64_t)std::max(1, select_resident<QT, D, THREADS>(ring + per * 4)) * sms;
+    const int64_t slots = select_resident<QT, D, THREADS>(ring + per * 4) * sms;
     const int64_t cost = (units * a.Hkv * n + slots - 1) / slots * ((per + THREADS - 1) / THREADS + 10);
     if (cost < least) {
       least = cost;
