@@ -282,7 +282,7 @@ struct SelectArgs {
   const void *q;
   const unsigned char *summaries;
   const int32_t *table, *starts, *lens;
-  int num_seqs, num_tokens, max_pages, Hkv, G;
+  int num_seqs, num_tokens, max_pages, Hkv, G, log_g;
   int64_t num_pages;
   int budget, sink_pages, local_pages;
   int32_t *selected;
@@ -392,82 +392,94 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   // the tokens that it lacks.
   constexpr int QL = D / QN;  // 16-byte words of a query; a lane's stand at the same dims
   static_assert(QL <= 32, "a row fits a warp");
-  const int rows = tokens * a.G, last_weight = first > 0 ? 1 + TU - tokens : 1;
-  auto load = [&](int row, float *f) {
-    const int tok = t0 + row / a.G, head = g * a.G + row % a.G;
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(
-        static_cast<const unsigned char *>(a.q) + (((int64_t)tok * a.Hkv * a.G + head) * D) * QB) + lane % QL);
-    widen<QT>(x, f);
+  const int rows = tokens << a.log_g;
+  const float last_weight = first > 0 ? (float)(1 + TU - tokens) : 1.f;
+  auto load = [&](int row) {  // (zeros past the last one)
+    if (row >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    const int64_t head = ((int64_t)(t0 + (row >> a.log_g)) * a.Hkv + g << a.log_g) + (row & (a.G - 1));
+    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(a.q) + head * (D * QB)) + lane % QL);
   };
-  int up[QN] = {}, down[QN] = {};
-  auto add = [&](const float *f, float factor, int weight) {
+  // The largest magnitude of the words seen, word by word, NaN where there was one.
+  uint32_t high[4] = {0u, 0u, 0u, 0u};
+  auto raise = [&](const uint4 &x) {
+    constexpr uint32_t kMagnitude = QT == KEYS_F32 ? 0x7fffffffu : 0x7fff7fffu;
+    high[0] = larger<QT>(high[0], x.x & kMagnitude);
+    high[1] = larger<QT>(high[1], x.y & kMagnitude);
+    high[2] = larger<QT>(high[2], x.z & kMagnitude);
+    high[3] = larger<QT>(high[3], x.w & kMagnitude);
+  };
+  auto highest = [&](bool &fine) {  // over the warp
+    float f[QN], most = 0.f;
+    widen<QT>(make_uint4(high[0], high[1], high[2], high[3]), f);
+    fine = true;
 #pragma unroll
     for (int e = 0; e < QN; ++e) {
-      const int x = weight * whole(f[e], factor);
-      up[e] += max(x, 0);
-      down[e] += max(-x, 0);
-    }
-  };
-  auto join_lanes = [&] {  // those of a warp at the same dims
-#pragma unroll
-    for (int e = 0; e < QN; ++e)
-#pragma unroll
-      for (int o = QL; o < 32; o <<= 1) {
-        up[e] += __shfl_xor_sync(0xffffffffu, up[e], o);
-        down[e] += __shfl_xor_sync(0xffffffffu, down[e], o);
-      }
-  };
-  int8_t *codes = s_codes[warp];
-  if (tokens == 1) {
-    // a single token: every warp for itself, nothing to wait for
-    constexpr int MOST = 8 * QL / 32;  // rows of a lane: 8 heads at most
-    float f[MOST][QN], most = 0.f;
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < MOST; ++i) {
-      const int row = i * (32 / QL) + lane / QL;
-#pragma unroll
-      for (int e = 0; e < QN; ++e) f[i][e] = 0.f;
-      if (row < rows) load(row, f[i]);
-#pragma unroll
-      for (int e = 0; e < QN; ++e) {
-        fine &= fabsf(f[i][e]) < INFINITY;
-        most = fmaxf(most, fabsf(f[i][e]));
-      }
+      fine &= f[e] < INFINITY;
+      most = fmaxf(most, f[e]);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float factor = whole_factor(most, __all_sync(0xffffffffu, fine));
+    fine = __all_sync(0xffffffffu, fine);
+    return most;
+  };
+  // Sums of the whole numbers and of their magnitudes, in fp32: at most 127 * 256
+  // rows, exact.  (Rounding to a whole number by adding 1.5 * 2^23.)
+  float sum[QN] = {}, size[QN] = {};
+  auto add = [&](const uint4 &x, float factor, float weight) {
+    constexpr float kRound = 12582912.f;
+    float f[QN];
+    widen<QT>(x, f);
 #pragma unroll
-    for (int i = 0; i < MOST; ++i) add(f[i], factor, last_weight);
+    for (int e = 0; e < QN; ++e) {
+      const float c = __fadd_rn(__fadd_rn(__fmul_rn(f[e], factor), kRound), -kRound);
+      sum[e] = fmaf(c, weight, sum[e]);
+      size[e] = fmaf(fabsf(c), weight, size[e]);
+    }
+  };
+  int up[QN], down[QN];
+  auto join_lanes = [&] {  // those of a warp at the same dims
+#pragma unroll
+    for (int e = 0; e < QN; ++e) {
+#pragma unroll
+      for (int o = QL; o < 32; o <<= 1) {
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+        size[e] += __shfl_xor_sync(0xffffffffu, size[e], o);
+      }
+      up[e] = (int)(0.5f * (size[e] + sum[e]));
+      down[e] = (int)(0.5f * (size[e] - sum[e]));
+    }
+  };
+  if (tokens == 1) {
+    // a single token: every warp for itself, nothing to wait for
+    constexpr int MOST = 8 * QL / 32;  // rows of a lane: 8 heads at most
+    uint4 x[MOST];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) x[i] = load(i * (32 / QL) + lane / QL);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) raise(x[i]);
+    bool fine;
+    const float most = highest(fine), factor = whole_factor(most, fine);
+    if (factor != 0.f) {  // (0: all codes 0, whatever the queries hold)
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) add(x[i], factor, last_weight);
+    }
     join_lanes();
   } else {
     constexpr int STEP = THREADS / QL;  // rows of the CTA at a time
     const int row0 = warp * (32 / QL) + lane / QL;
-    float most = 0.f;
-    bool fine = true;
 #pragma unroll 4
-    for (int row = row0; row < rows; row += STEP) {
-      float f[QN];
-      load(row, f);
-#pragma unroll
-      for (int e = 0; e < QN; ++e) {
-        fine &= fabsf(f[e]) < INFINITY;
-        most = fmaxf(most, fabsf(f[e]));
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int row = row0; row < rows; row += STEP) raise(load(row));
+    bool fine;
+    float most = highest(fine);
     if (lane == 0) s_red[warp][0] = __float_as_int(most);
     for (int i = tid; i < 2 * D; i += THREADS) s_sums[i] = 0;
     fine = __syncthreads_and(fine);
     for (int w = 0; w < WARPS; ++w) most = fmaxf(most, __int_as_float(s_red[w][0]));
     const float factor = whole_factor(most, fine);
+    if (factor != 0.f) {
 #pragma unroll 4
-    for (int row = row0; row < rows; row += STEP) {
-      float f[QN];
-      load(row, f);
-      add(f, factor, row / a.G == tokens - 1 ? last_weight : 1);
+      for (int row = row0; row < rows; row += STEP)
+        add(load(row), factor, row >> a.log_g == tokens - 1 ? last_weight : 1.f);
     }
     join_lanes();
     if (lane < QL) {
@@ -484,6 +496,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
       down[e] = s_sums[D + lane % QL * QN + e];
     }
   }
+  int8_t *codes = s_codes[warp];
   {
     int top = 0;
 #pragma unroll
@@ -874,6 +887,7 @@ extern "C" int cpa_select_pages(const void *q, const void *summaries, const int3
   a.max_pages = desc->max_pages_per_seq;
   a.Hkv = desc->num_kv_heads;
   a.G = desc->num_q_heads / desc->num_kv_heads;
+  a.log_g = a.G == 1 ? 0 : a.G == 2 ? 1 : a.G == 4 ? 2 : 3;  // (check_shape: no others)
   a.num_pages = desc->num_pages;
   a.budget = num_selected;
   a.sink_pages = sink_pages;
