@@ -113,7 +113,11 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.num_seqs;
   auto pages_of = [&](int s, int &first) {
     const int q = __ldg(a.starts + s + 1) - __ldg(a.starts + s);
-    const int len = min(__ldg(a.lens + s), a.max_pages * kPageTokens);
+    int len = __ldg(a.lens + s);
+    if (len > a.max_pages * kPageTokens) {
+      if (a.status) atomicOr(a.status, STATUS_BAD_PAGE);
+      len = a.max_pages * kPageTokens;
+    }
     first = max(0, len - q) / kPageTokens;
     return q > 0 && len >= q ? len / kPageTokens - first : 0;
   };
@@ -786,6 +790,7 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
       nc = n;
     }
   }
+  if (units * a.Hkv * nc > INT32_MAX) return cudaErrorInvalidConfiguration;
   a.capacity = (a.max_pages + nc - 1) / nc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * a.Hkv * nc));
@@ -832,6 +837,7 @@ extern "C" int cpa_summarise_pages(const void *k_cache, const int32_t *block_tab
   if (num_seqs == 0) return CPA_OK;
   if (!k_cache || !summaries || !aligned(k_cache, 16) || !aligned(summaries, 16)) return CPA_ERR_ARG;
   if ((rc = check_batch(desc, num_seqs, block_table, query_start_loc, seq_lens)) != CPA_OK) return rc;
+  if ((int64_t)num_seqs * desc->max_pages_per_seq > INT32_MAX) return CPA_ERR_UNSUPPORTED;
   SummariseArgs a{};
   if ((rc = status_of(desc, &a.status)) != CPA_OK) return rc;
   a.k_cache = static_cast<const unsigned char *>(k_cache);

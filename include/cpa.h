@@ -380,7 +380,7 @@ size_t cpa_summary_bytes(const cpa_desc *desc);
  * (seq_lens[s] - q_len) div 16 .. seq_lens[s] div 16 - 1 of every sequence, whose
  * keys are in the cache (cpa_kv_append, or an attention call with the append).  To
  * make the summaries of whole sequences anew, describe them as chunks of all their
- * tokens.  For keys K[t][d] of a page and kv head, in fp32 (an E4M3 cache: the
+ * tokens (num_seqs * max_pages_per_seq is below 2^31, CPA_ERR_UNSUPPORTED).  For keys K[t][d] of a page and kv head, in fp32 (an E4M3 cache: the
  * codes' values, without the scale):
  *   a = max |K|,  f = 127 / a,  scale = a / 127,
  *   hi[d] = round(f * max_t K[t][d]),  lo[d] = round(f * min_t K[t][d]),
@@ -414,7 +414,7 @@ int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *nu
  * behind all others and raises the status word.  Every candidate's summary must
  * have been made.  A context of at most num_selected candidates reads none.
  * sink_pages >= 0, num_selected >= 0 (0: nothing to do); max_pages_per_seq at most
- * 262144 (CPA_ERR_UNSUPPORTED). */
+ * 262144, num_pages * num_kv_heads below 2^31 (CPA_ERR_UNSUPPORTED). */
 int cpa_select_pages(const void *q, const void *summaries, const int32_t *block_table,
                      const int32_t *query_start_loc, const int32_t *seq_lens, int32_t num_seqs,
                      int32_t num_selected, int32_t sink_pages, int32_t local_pages,

@@ -188,6 +188,19 @@ def test_many_rows(cuda_device):
     run_select(q, rows, where, table, [1] * 4000, lens, 8, 1, 2, cuda_device)
 
 
+@pytest.mark.parametrize("hq", [1, 8])
+def test_units_of_long_chunks(cuda_device, hq):
+    """Many units per chunk, chunks that begin and end anywhere, short last units of one token and of all but one."""
+    size = 256 // hq
+    q_lens = [3 * size + 1, 1, 5 * size - 1, 2 * size, size + 1, 1, 2000, size - 1]
+    seq_lens = [q + o for q, o in zip(q_lens, [700, 90, 0, 1300, 15, 800, 333, 2000])]
+    pages = sum(-(-n // PAGE) for n in seq_lens)
+    rows = random_rows(pages, 1, 64, 24)
+    table, where = step_tensors(q_lens, seq_lens, pages, 25, cuda_device)
+    q = torch.randn(sum(q_lens), hq, 64, generator=torch.Generator().manual_seed(26)).bfloat16().to(cuda_device)
+    run_select(q, rows, where, table, q_lens, seq_lens, 6, 1, 2, cuda_device)
+
+
 def test_bad_entries_raise_the_status_word(cuda_device):
     rows = random_rows(60, 2, 64, 16)
     table, where = step_tensors([1, 1], [500, 400], 60, 17, cuda_device)
@@ -206,6 +219,9 @@ def test_bad_entries_raise_the_status_word(cuda_device):
     assert int(ws[0]) == 1 and int(selected.max()) < table.shape[1]
     cache = random_cache(60, 2, 64, "bf16", 19, cuda_device)
     summaries = ops.summaries_for(cache)
+    ws.zero_()
+    ops.summarise_pages(cache, *where, summaries, workspace=ws)   # (none of the table's pages is completed)
+    assert int(ws[0]) == 1 and not summaries.any()
     ws.zero_()
     ops.summarise_pages(cache, where[0], starts_of([500, 300]).to(cuda_device), torch.tensor([500, 400], dtype=torch.int32, device=cuda_device), summaries, workspace=ws)
     assert int(ws[0]) == 1

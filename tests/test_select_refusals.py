@@ -67,6 +67,7 @@ def test_selection_refuses():
     assert choose(sum=OFF8) == choose(q=OFF8) == choose(sel=ODD) == choose(bt=ODD) == ops.CPA_ERR_ARG
     assert choose(desc(max_pages_per_seq=0)) == ops.CPA_ERR_ARG
     assert choose(desc(max_pages_per_seq=262145)) == choose(desc(num_pages=1 << 27)) == choose(desc(page_size=32)) == ops.CPA_ERR_UNSUPPORTED
+    assert choose(desc(num_pages=1 << 26, num_kv_heads=32)) == ops.CPA_ERR_UNSUPPORTED
     assert choose(desc(num_tokens=5000), n=4097) == ops.CPA_ERR_UNSUPPORTED
     assert choose(desc(workspace=4100, workspace_bytes=256)) == choose(desc(workspace=4096, workspace_bytes=64)) == ops.CPA_ERR_WORKSPACE
     assert choose(pages=0, sel=None) == choose(desc(num_tokens=0)) == choose(n=0) == ops.CPA_OK
@@ -77,6 +78,7 @@ def test_summaries_refuse():
         assert summary(**{name: None}) == ops.CPA_ERR_ARG, name
     assert summary(kc=OFF8) == summary(sum=OFF8) == summary(qsl=ODD) == summary(n=-1) == ops.CPA_ERR_ARG
     assert summary(n=4097) == summary(desc(head_dim=80)) == summary(desc(max_pages_per_seq=(1 << 26) + 1)) == ops.CPA_ERR_UNSUPPORTED
+    assert summary(desc(max_pages_per_seq=1 << 22), n=512) == ops.CPA_ERR_UNSUPPORTED
     assert summary(desc(workspace=4096, workspace_bytes=64)) == ops.CPA_ERR_WORKSPACE
     assert summary(n=0) == ops.CPA_OK
     copy = lambda s, d, n, m, at, ds: ops.cpa_copy_summaries(s, d, n, m, at, ds, None)  # noqa: E731
