@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   int *sq_qs = plan_smem, *sq_len = sq_qs + S, *sq_ctx = sq_len + S;
   int *s_dec = sq_ctx + S;     // [S + 1] exclusive bases of each sequence's slices
   int *s_chk = s_dec + S + 1;  // [S + 1] ... and of its chunk units
-  int *s_pos = s_chk + S + 1;  // [S] first place of a decode sequence's slices, by size
+  int *s_pos = s_chk + S + 1;  // [S] first place of a decode sequence's slices, by size;
+                               // over lists: into how many units a chunk's pairs are split
   __shared__ long long s_red[kPlanWorkers / 32][3];
   __shared__ int s_wd[kPlanWorkers / 32], s_wc[kPlanWorkers / 32];
   __shared__ int s_hist[kSizeBuckets];
@@ -376,8 +377,30 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   const int nu = (tq == 0 || tq >= grid) ? 1 : (int)max(1ll, (long long)kMaxStepGrid / tq);
   const int unit_tiles =
       (int)max((long long)kMinUnitTiles, ((tt + (tp + 7) / 8 + grid - 1) / grid * 3 + 3) / 4);
+  // Over lists all pairs are about as long, and short: split into k units, a pair
+  // takes a unit's tiles, and a merge of 3 + k tiles' time, in as many rounds as the
+  // units fill the grid; never less than all units' and slices' share.  (2048-key
+  // lists, 8 kv heads of 128, binary16; this rule against the one above, us: chunks
+  // of 256 / 512 / 768 / 1024 tokens 36 / 42 / 49 / 52 against 36 / 52 / 66 / 78; 512
+  // tokens beside 8 / 16 / 32 single tokens of 68 pages, the whole step 63 / 76 / 81
+  // against 72 / 73 / 86.)
+  auto split = [&](int t) {
+    int best = 1, least = INT32_MAX;
+    const int slices = (int)min(tp / 12, 1ll << 24);
+    for (int k = 1; k <= min(nu, min(t, 8)); ++k) {
+      const int size = ceil_div(t, k) + (k > 1 ? 3 + k : 0), all = (int)tq * k;  // (tq < grid where k > 1)
+      const int cost = k == 1 && tq >= grid ? 0
+                                            : max(ceil_div(all, w.grid) * size, (all * size + slices) / w.grid);
+      if (cost < least) {
+        least = cost;
+        best = k;
+      }
+    }
+    return best;
+  };
   auto units = [&](int s) {  // chunk units of one kv head of sequence s
     const int mt = ceil_div(sq_len[s] * G, BM), npair = (mt + 1) / 2;
+    if (VIS == kSelected) return npair * s_pos[s];  // (found in pass 2)
     return npair * min(nu, ceil_div(pair_kv<G, VIS>(p, sq_ctx[s], sq_len[s], npair - 1, mt), unit_tiles));
   };
   auto dec_pages = [&](int s) { return ceil_div(decode_ctx<VIS>(p, sq_ctx[s]), kPage); };
@@ -398,6 +421,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
       cd += n;
       atomicAdd(&s_hist[bucket(s)], n);
     } else if (sq_len[s] > 1) {
+      if (VIS == kSelected) {
+        const int mt = ceil_div(sq_len[s] * G, BM);
+        s_pos[s] = split(pair_kv<G, VIS>(p, sq_ctx[s], sq_len[s], (mt + 1) / 2 - 1, mt));
+      }
       cc += Hkv * units(s);
     }
   }
