@@ -10,6 +10,8 @@
   appends pages, ``ceil(len / 16)`` in total.
 * ``slot_mapping`` (int64 [T]): cache slot page * page_size + offset of each
   new token, consumed by ``cpa_kv_append``.
+
+(On the device, from a page table of all requests: ``ops.pack_step``.)
 """
 from __future__ import annotations
 

@@ -30,7 +30,11 @@ constexpr float kTiny = 0x1p-100f;  // smaller magnitudes count as zero: 127 / x
 
 // ---------------------------------------------------------------------------
 // Summaries.  A warp makes one page's row of one kv head: the lanes of a row of
-// keys hold 16 bytes of it each, and the groups of lanes take different keys.
+// keys hold 16 bytes of it each, and the groups of lanes take different keys.  The
+// extremes are taken in the keys' own 16 bits, two to an instruction, and the next
+// page's keys are on their way meanwhile.  (8 prompts of 8192 tokens, 8 kv heads of
+// 128, bf16: 134 MB in 25 us, 5.4 TB/s; element by element in fp32, without the next
+// page's loads, 33 us.  The pages' places are looked up 32 at a time, a lane each.)
 constexpr int kSumThreads = 256;
 
 enum { KEYS_BF16 = 0, KEYS_F16 = 1, KEYS_E4M3 = 2, KEYS_F32 = 3 };
