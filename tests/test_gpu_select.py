@@ -178,6 +178,19 @@ def test_long_contexts_and_wide_tables(cuda_device, length, columns):
             run_select(q, rows, where, table, q_lens, [length], budget, 1, local, cuda_device)
 
 
+def test_summaries_beyond_32_bit_offsets(cuda_device):
+    rows = random_rows(100, 8, 128, 27)
+    far = 2 ** 32 // (8 * 272) + 10
+    table, where = step_tensors([1, 30], [1000, 500], 100, 28, cuda_device)
+    pool = torch.empty(far + 100, 8, 272, dtype=torch.uint8, device=cuda_device)
+    pool[far:] = torch.as_tensor(rows).to(cuda_device)
+    q = torch.randn(31, 16, 128, generator=torch.Generator().manual_seed(29)).bfloat16().to(cuda_device)
+    got = torch.full((31, 8, 5), -7, dtype=torch.int32, device=cuda_device)
+    ops.select_pages(q, pool, torch.where(where[0] >= 0, where[0] + far, -1), *where[1:], got, sink_pages=1, local_pages=2)
+    want = select(q, rows, table, [1, 30], [1000, 500], 5, 1, 2, np.full(got.shape, -7, np.int32))
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_many_rows(cuda_device):
     """More units than the GPU holds at a time; 4000 sequences."""
     lens = [40 + 7 * (i % 90) for i in range(4000)]

@@ -142,6 +142,21 @@ def test_results_do_not_vary(cuda_device):
         assert torch.equal(call(b).view(torch.int16), first.view(torch.int16))
 
 
+@pytest.mark.parametrize("mode", ["bf16", "bf16-e4m3", "f32"])
+def test_pages_beyond_32_bit_offsets(cuda_device, mode):
+    """A pool of more than 2^32 bytes in each cache, the batch's pages at its end, for every kernel."""
+    for q_lens in ([1, 1, 1], [1, 40, 1]):
+        b = make_batch(q_lens, [500, 700, 300], 16, 8, 128, mode, 6, 2, 16, cuda_device)
+        pages = b["k_cache"].shape[0]
+        far = 2 ** 32 // (b["k_cache"][0].numel() * b["k_cache"].element_size()) + 10
+        for c in ("k_cache", "v_cache"):
+            pool = torch.empty(far + pages, *b[c].shape[1:], dtype=b[c].dtype, device=cuda_device)
+            pool[far:] = b[c]
+            b[c] = pool
+        b["table"] = torch.where(b["table"] >= 0, b["table"] + far, -1)
+        check(b)
+
+
 def test_rows_behind_the_last_token_are_left(cuda_device):
     b = make_batch([1, 33, 1], [100, 200, 300], 8, 2, 64, "bf16", 4, 1, 14, cuda_device)
     big = torch.full((b["q"].shape[0] + 9, 8, 64), 7.0, dtype=torch.bfloat16, device=cuda_device)
