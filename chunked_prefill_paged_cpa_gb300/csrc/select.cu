@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(const SummariseA
 // and 256 threads 71, 67 and 88 us, and a hybrid step's selection, where a chunk's
 // units take longest, 40, 35 and 33 us against 28; clusters of two 102 us.)
 // A single unit waits for its chain: metadata, entries, summaries, then five or six
-// barriers of the cluster (6250 pages, 8 kv heads: 13.6 us; 63 us before every lane
+// barriers of the cluster (6247 pages, 8 kv heads: 13 us; 63 us before every lane
 // fetched another CTA's counts).
 constexpr int kSelThreads = 128, kWideThreads = 256;
 constexpr int kDigits = 256;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   __shared__ int s_sums[2 * D];
   __shared__ __align__(16) int8_t s_codes[WARPS][2 * D];
   __shared__ int s_red[WARPS][3];
-  // (once the scores are there, in the rings' place)
+  // (once the scores are there, in the summaries' place)
   int(*s_hist)[kDigits] = reinterpret_cast<int(*)[kDigits]>(sm_select), *s_all = s_hist[4];
   __shared__ uint32_t s_range[3];  // this CTA's ordinary keys: least, largest; its top keys
   __shared__ int s_more[2];        // this CTA's keys above the threshold, and at it
@@ -376,20 +376,20 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     if (a.status) atomicOr(a.status, STATUS_BAD_PAGE);
     return -1;
   };
-  uint4 *ring = sm_select + warp * 32 * CH;
+  uint4 *mine32 = sm_select + warp * 32 * CH;  // the warp's 32 summaries
   // 32 summaries on their way: the codes of 32 / CL of them at a time, consecutive
   // lanes taking consecutive 16 bytes, then a scale for each lane
   constexpr int CL = CH - 1;
   auto fetch = [&](int entry) {
     const unsigned char *from = a.summaries + (lane % CL) * 16;
-    uint4 *to = ring + lane / CL * CH + lane % CL;
+    uint4 *to = mine32 + lane / CL * CH + lane % CL;
     const int mine = entry < 0 ? -1 : entry * a.Hkv + g;  // (at most num_pages Hkv - 1, see the host's checks)
 #pragma unroll
     for (int i = 0; i < CL; ++i) {
       const int row = __shfl_sync(0xffffffffu, mine, i * (32 / CL) + lane / CL);
       ptx::cp_async16(to + i * (32 / CL) * CH, from + (int64_t)max(row, 0) * ROW_BYTES, row < 0 ? 0 : 16);
     }
-    ptx::cp_async16(ring + lane * CH + CL, a.summaries + (int64_t)max(mine, 0) * ROW_BYTES + 2 * D, mine < 0 ? 0 : 16);
+    ptx::cp_async16(mine32 + lane * CH + CL, a.summaries + (int64_t)max(mine, 0) * ROW_BYTES + 2 * D, mine < 0 ? 0 : 16);
     ptx::cp_async_commit();
   };
   int entry = look_up(j0 + warp * 32), next = look_up(j0 + warp * 32 + THREADS);
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   for (int j = j0 + warp * 32; j < j1; j += THREADS) {
     ptx::cp_async_wait<0>();
     __syncwarp();
-    const uint4 *row = ring + lane * CH;
+    const uint4 *row = mine32 + lane * CH;
     int sum[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < CH - 1; ++i) {
@@ -561,7 +561,10 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   least = __reduce_min_sync(0xffffffffu, least);
   largest = __reduce_max_sync(0xffffffffu, largest);
   tops = __reduce_add_sync(0xffffffffu, tops);
-  __syncthreads();  // (s_red and the rings have been read)
+  // (a warp without a page has not waited for its fetch of zeros; the counts take
+  // the summaries' place)
+  ptx::cp_async_wait<0>();
+  __syncthreads();  // (s_red and the summaries have been read)
   for (int i = tid; i < 4 * kDigits; i += THREADS) s_hist[0][i] = 0;
   if (lane == 0) {
     s_red[warp][0] = (int)least;
@@ -730,7 +733,7 @@ int check_batch(const cpa_desc *d, int num_seqs, const void *table, const void *
 
 template <int KT, int D>
 cudaError_t launch_summarise(const SummariseArgs &a, int sms, cudaStream_t stream) {
-  // (48 KB of shared memory at most: 4097 words)
+  // (16 KB of shared memory at most: 4097 words)
   const size_t smem = sizeof(int) * ((size_t)a.num_seqs + 1);
   // as many CTAs as are resident at once
   static PerDevice ctas;
@@ -769,8 +772,8 @@ constexpr int kSharedLimit = 216 * 1024;  // beside the static part
 
 template <int QT, int D, int THREADS>
 cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t stream) {
-  constexpr int ring = THREADS * (2 * D + 16);
-  static_assert(ring >= 5 * kDigits * 4, "the counts fit the rings");
+  constexpr int room = THREADS * (2 * D + 16);  // for the summaries
+  static_assert(room >= 5 * kDigits * 4, "the counts fit in the summaries' place");
   const int device = current_device();
   static PerDevice configured;
   cudaError_t e = cudaSuccess;
@@ -786,8 +789,8 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
   int64_t least = INT64_MAX;
   for (int n = 1; n <= kMaxCluster; n *= 2) {
     const int per = (a.max_pages + n - 1) / n;
-    if (per > kMaxScores || ring + per * 4 > kSharedLimit) continue;
-    const int64_t slots = select_resident<QT, D, THREADS>(ring + per * 4) * sms;
+    if (per > kMaxScores || room + per * 4 > kSharedLimit) continue;
+    const int64_t slots = select_resident<QT, D, THREADS>(room + per * 4) * sms;
     const int64_t cost = (units * a.Hkv * n + slots - 1) / slots * ((per + THREADS - 1) / THREADS + 10);
     if (cost < least) {
       least = cost;
@@ -799,7 +802,7 @@ cudaError_t launch_select_on(SelectArgs a, int64_t units, int sms, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * a.Hkv * nc));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = ring + (size_t)a.capacity * 4;
+  cfg.dynamicSmemBytes = room + (size_t)a.capacity * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

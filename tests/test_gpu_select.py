@@ -178,6 +178,19 @@ def test_long_contexts_and_wide_tables(cuda_device, length, columns):
             run_select(q, rows, where, table, q_lens, [length], budget, 1, local, cuda_device)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_fewer_pages_than_a_cluster_has_warps(cuda_device, d):
+    """CTAs and warps without a page beside others with some."""
+    for length in (100, 300, 520, 900, 2300):
+        pages = -(-length // PAGE)
+        rows = random_rows(pages, 1, d, length)
+        table, where = step_tensors([1], [length], pages, 30, cuda_device, 20000)
+        q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(31)).bfloat16().to(cuda_device)
+        for budget in (1, 3, 17):
+            for _ in range(5):
+                run_select(q, rows, where, table, [1], [length], budget, 1, 2, cuda_device)
+
+
 def test_summaries_beyond_32_bit_offsets(cuda_device):
     rows = random_rows(100, 8, 128, 27)
     far = 2 ** 32 // (8 * 272) + 10
