@@ -1,5 +1,5 @@
 // Attention of a batch of single tokens that see a window, or selected pages, with
-// 16-bit queries: one launch, no plan.
+// 16-bit queries, or selected pages in fp32: one launch, no plan.
 //
 // Either way every row sees about the same number of keys and the host knows a
 // bound on it, so the step kernel's queue has nothing to balance.  Work
@@ -17,12 +17,20 @@
 // the tcgen05 rate, but a page costs about 120 of a warp's instructions, and
 // nothing waits: no barrier, no shared memory until the warps' states are
 // joined at the end (through shared memory, then the cluster's).
+//
+// fp32 (KVM 3): m16n8k8 with every operand as two tf32 values (tf32_split.cuh), Q's
+// halves in shared memory, P turned by shuffles.  A page is some 900 instructions,
+// and as keys are the 16 rows of S and dims those of O^T, each element of K and V
+// is split once.  (8 kv heads of 128 with 4 query heads each, 68 pages: 20 / 60
+// tokens 49 / 102 us, 5.1 TB/s; on the kernel of mixed fp32 steps, whose 16 rows a
+// token fills with its 4, 65 / 128 us.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
 
 #include "cpa_internal.cuh"
 #include "ptx.cuh"
+#include "tf32_split.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -72,12 +80,12 @@ __device__ __forceinline__ uint2 load8(const unsigned char *p) {
 // c = lane % 4: of K, rows r and r + 8, 16 bytes of each 64 (at 16 c); of V,
 // rows 2c, 2c + 1, 2c + 8 and 2c + 9, the dims r D / 8 .. (r + 1) D / 8 - 1.
 // (Of V in 16 bits a lane could take 16 bytes of each 128 instead, so that every
-// load reads whole lines: measured 1.5 % slower.)
+// load reads whole lines: measured 1.5 % slower.  Of V in fp32 it does.)
 template <int KVM, int D>
 struct PageRegs {
-  static constexpr int EB = KVM == 2 ? 1 : 2;
+  static constexpr int EB = KVM == 2 ? 1 : KVM == 3 ? 4 : 2;
   static constexpr int KC = D * EB / 64;   // 16-byte words per row of K
-  static constexpr int VW = D * EB / 32;   // 4-byte words per row of V: 2, 4 or 8
+  static constexpr int VW = D * EB / 32;   // 4-byte words per row of V: 2 .. 16
   uint32_t k[2][KC * 4];
   uint32_t v[4][VW];
 
@@ -96,7 +104,8 @@ struct PageRegs {
   __device__ __forceinline__ void load_v(const unsigned char *vp, int r, int c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const unsigned char *row = vp + (2 * c + (j & 1) + 8 * (j >> 1)) * (D * EB) + r * (VW * 4);
+      const unsigned char *row =
+          vp + (2 * c + (j & 1) + 8 * (j >> 1)) * (D * EB) + r * (KVM == 3 ? 16 : VW * 4);
       if constexpr (VW == 2) {
         const uint2 x = load8(row);
         v[j][0] = x.x;
@@ -104,7 +113,7 @@ struct PageRegs {
       } else {
 #pragma unroll
         for (int i = 0; i < VW / 4; ++i) {
-          const uint4 x = load16(row + i * 16);
+          const uint4 x = load16(row + i * (KVM == 3 ? 128 : 16));
           v[j][4 * i] = x.x;
           v[j][4 * i + 1] = x.y;
           v[j][4 * i + 2] = x.z;
@@ -118,8 +127,9 @@ struct PageRegs {
 template <int KVM, int D, int W, int VIS>
 __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams p) {
   constexpr bool F16 = KVM != 0;
-  constexpr int EB = KVM == 2 ? 1 : 2;
-  constexpr int KS = D / 16;   // k-steps of S, and 16-dim tiles of O^T
+  constexpr int EB = KVM == 2 ? 1 : KVM == 3 ? 4 : 2;
+  constexpr int KS = D / 16;   // k-steps of S (of 8 dims in fp32: twice as many), and 16-dim tiles of O^T
+  __shared__ uint2 sm_q[KVM == 3 ? 2 * KS * 64 : 1];  // fp32: [k-step][hi, lo][lane]
   using Page = PageRegs<KVM, D>;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = blockIdx.x, nc = gridDim.x, g = blockIdx.y;
@@ -180,8 +190,23 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
 
   // Q as the B operand: head r, the dims that K's lanes with this c hold, in
   // the order in which the k-steps use them
-  uint32_t qb[KS][2];
-  {
+  uint32_t qb[KVM == 3 ? 1 : KS][2];
+  if constexpr (KVM == 3) {
+    for (int i = threadIdx.x; i < 2 * KS * 32; i += W * 32) {
+      const int ks = i / 32, l = i % 32, head = l >> 2;
+      const int dim = (ks >> 1) * 16 + (l & 3) * 4 + (ks & 1) * 2;
+      float2 x = make_float2(0.f, 0.f);
+      if (head < G && vis > 0)
+        x = __ldg(reinterpret_cast<const float2 *>(static_cast<const float *>(p.q) +
+                                                   ((int64_t)t * p.Hq + g * G + head) * D + dim));
+      uint2 hi, lo;
+      split(x.x, hi.x, lo.x);
+      split(x.y, hi.y, lo.y);
+      sm_q[ks * 64 + l] = hi;
+      sm_q[ks * 64 + 32 + l] = lo;
+    }
+    __syncthreads();
+  } else {
     const bool have = r < G && vis > 0;
     const unsigned short *q =
         static_cast<const unsigned short *>(p.q) + ((int64_t)t * p.Hq + g * G + (r < G ? r : 0)) * D;
@@ -240,8 +265,23 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
   // Page v, held in x: S, then after_s(); softmax and O, then after_o().
   auto page = [&](Page &x, int v, int e, auto after_s, auto after_o) {
     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (KVM == 3) {
+      float small[2][4] = {};  // hi lo, lo hi
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
+      for (int ks = 0; ks < 2 * KS; ++ks) {
+        const uint2 qh = sm_q[ks * 64 + lane], ql = sm_q[ks * 64 + 32 + lane];
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split(__uint_as_float(x.k[e & 1][2 * ks + (e >> 1)]), h[e], l[e]);
+        mma_tf32((ks & 1) ? sb : sa, h[0], h[1], h[2], h[3], qh.x, qh.y);
+        mma_tf32(small[0], h[0], h[1], h[2], h[3], ql.x, ql.y);
+        mma_tf32(small[1], l[0], l[1], l[2], l[3], qh.x, qh.y);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sa[e] += small[0][e] + small[1][e];
+    }
+#pragma unroll
+    for (int ks = 0; ks < (KVM == 3 ? 0 : KS); ++ks) {
       uint32_t a[4];
       if constexpr (KVM == 2) {
         ptx::e4m3x4_to_f16x4(x.k[0][ks], a[0], a[2]);
@@ -304,6 +344,30 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
     const float p2 = ptx::ex2(sc[2] - r0), p3 = ptx::ex2(sc[3] - r1);
     l0 += p0 + p2;
     l1 += p1 + p3;
+    if constexpr (KVM == 3) {
+      // P^T as the B operand: head r, keys 2c and 2c + 1, then 8 more of each
+      const int from = 8 * c + (r >> 1);
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float even = __shfl_sync(0xffffffffu, j < 2 ? p0 : p2, from + 4 * (j & 1));
+        const float odd = __shfl_sync(0xffffffffu, j < 2 ? p1 : p3, from + 4 * (j & 1));
+        split((r & 1) ? odd : even, ph[j], pl[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; m += 2) {
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split(__uint_as_float(x.v[m + (e >> 1)][2 * i + (e & 1)]), h[e], l[e]);
+          mma_tf32(o[i], h[0], h[1], h[2], h[3], pl[m], pl[m + 1]);
+          mma_tf32(o[i], l[0], l[1], l[2], l[3], ph[m], ph[m + 1]);
+          mma_tf32(o[i], h[0], h[1], h[2], h[3], ph[m], ph[m + 1]);
+        }
+      after_o();
+      return;
+    }
     const uint32_t b0 = transpose8(F16 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1));
     const uint32_t b1 = transpose8(F16 ? ptx::pack_f16x2(p2, p3) : ptx::pack_bf16x2(p2, p3));
     // O^T tile i: dims 2i and 2i + 1 of those that the lane holds (rows r and r + 8)
@@ -332,8 +396,9 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
   // K's words as soon as S has used K's registers, V's after O has used V's; the
   // registers saved hold a third more warps.  (256 and 64 tokens of 8 kv heads,
   // window 4096, head_dim 128: bf16 612 / 163 us with a second set, 619 / 206
-  // without; E4M3 337 / 120 and 341 / 87 us.)
-  if constexpr (KVM != 2) {
+  // without; E4M3 337 / 120 and 341 / 87 us.)  fp32: as 8-bit caches, since a second
+  // set does not fit.
+  if constexpr (KVM < 2) {
     auto none = [] {};
     auto fetch = [&](Page &x, int v) {
       int64_t at;
@@ -390,7 +455,7 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
   }
 #pragma unroll
   for (int i = 0; i < KS; ++i) {
-    const int dim = r * (D / 8) + 2 * i;
+    const int dim = KVM == 3 ? (i >> 1) * 32 + 4 * r + 2 * (i & 1) : r * (D / 8) + 2 * i;
     if (2 * c < G) *reinterpret_cast<float2 *>(&sm_o[warp][2 * c][dim]) = make_float2(o[i][0], o[i][2]);
     if (2 * c + 1 < G) *reinterpret_cast<float2 *>(&sm_o[warp][2 * c + 1][dim]) = make_float2(o[i][1], o[i][3]);
   }
@@ -413,6 +478,10 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
   auto store = [&](int h, int d, const State &x) {
     if (vis <= 0) return;  // a malformed row: not owned, or longer than its context
     const float y = KVM == 2 ? x.O * (p.v_scale / x.L) : x.O / x.L;
+    if (KVM == 3) {
+      static_cast<float *>(p.out)[((int64_t)t * p.Hq + g * G + h) * D + d] = y;
+      return;
+    }
     const bool f16 = KVM == 1 || (KVM == 2 && p.act_f16);
     static_cast<uint16_t *>(p.out)[((int64_t)t * p.Hq + g * G + h) * D + d] =
         f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
@@ -562,6 +631,9 @@ bool window_decode_beside(const AttnParams &p, int sms) {
 
 template <int VIS>
 static cudaError_t launch_seeing(const AttnParams &p, int sms, cudaStream_t stream) {
+  if constexpr (VIS == kSelected) {
+    if (p.act_f32) return p.D == 128 ? launch<3, 128, VIS>(p, sms, stream) : launch<3, 64, VIS>(p, sms, stream);
+  }
   if (p.D == 128) {
     if (p.kv_e4m3) return launch<2, 128, VIS>(p, sms, stream);
     return p.act_f16 ? launch<1, 128, VIS>(p, sms, stream) : launch<0, 128, VIS>(p, sms, stream);

@@ -6,11 +6,8 @@
 // of them.  A warp computes a tile against runs of 8 keys (half a page),
 //   S = Q K^T   m16n8k8, rows x keys
 //   O += P V    m16n8k8, rows x dims, one k-step of 8 keys
-// on the tensor cores with fp32's precision: every fp32 operand is the sum of
-// two tf32 values, x = hi + lo (11 significant bits each, rounded to nearest,
-// so |x - hi - lo| <= 2^-23 |x|), and a product is hi hi + hi lo + lo hi; the
-// term left out is below 2^-22 of the product.  Sums, softmax and outputs are
-// fp32.
+// on the tensor cores with fp32's precision, every operand as the sum of two tf32
+// values (tf32_split.cuh).  Sums, softmax and outputs are fp32.
 //
 // K and V go from global memory straight into the operands' registers; which
 // dim stands at which k, and which key of the eight, is free as long as the
@@ -32,6 +29,7 @@
 
 #include "cpa_internal.cuh"
 #include "ptx.cuh"
+#include "tf32_split.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -42,27 +40,6 @@ constexpr int kPageKeys = 16, kUnitKeys = 8;
 constexpr int kWarps = 4;
 constexpr int kRows = 16;
 constexpr float kMoveThreshold = 8.0f;  // log2 units, as in the step kernel
-
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// x as hi + lo, each rounded to tf32 (nearest, ties away; the tensor core
-// ignores the low 13 bits) by adding half a step to the bits.  In a NaN with all
-// its high bits set, the one that fp32 arithmetic here gives among them, that
-// addition would run over into the sign and leave a zero.  So what is not
-// finite, for which x - hi is NaN, keeps its NaN in lo: whatever it is
-// multiplied by is NaN.  (Test and selection cost up to 1 %: 4 tokens and a
-// 1000-token chunk, 8 kv heads of 128, window 1024 / 4096: 415 / 1450 us without,
-// 416 / 1460 with them; both roundings by cvt.rna.tf32, which keeps NaN, 453 / 1568.)
-__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  const float rest = x - __uint_as_float(hi);
-  lo = rest == rest ? __float_as_uint(rest) + 0x1000u : 0x7fffffffu;
-}
 
 // Eight keys of K and V of one kv head as a lane holds them.  With r = lane / 4
 // and c = lane % 4: of K, row r, 16 bytes of each 64 (at 16 c); of V, rows 2c

@@ -195,6 +195,7 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
   p.page_size = desc->page_size;
   p.num_pages = desc->num_pages;
   p.max_pages = desc->max_pages_per_seq;
+  p.act_f32 = desc->dtype == CPA_F32;
   p.act_f16 = desc->dtype == CPA_F16;
   p.kv_e4m3 = desc->kv_dtype == CPA_KV_E4M3;
   p.k_scale = p.kv_e4m3 ? desc->k_scale : 1.f;
@@ -233,7 +234,9 @@ int attention(const void *q, const void *k_cache, const void *v_cache,
     if (cudaMemsetAsync(desc->workspace, 0, clear_bytes, st) != cudaSuccess) return CPA_ERR_CUDA;
   }
   // with a window or selected pages: fp32 steps, and steps of one token per sequence
-  const bool single = w.step && limited && p.num_tokens == num_seqs && window_decode_takes(p, grid);
+  const bool single = p.num_tokens == num_seqs &&
+                      (w.step ? limited && window_decode_takes(p, grid)
+                              : sight.vis == kSelected && num_seqs <= kDecodeMaxSeqs);
   // a mixed step's single tokens beside the step kernel of its chunks
   const bool beside = w.step && limited && p.num_tokens > num_seqs && num_seqs > 1 &&
                       window_decode_beside(p, grid);

@@ -120,9 +120,11 @@ struct AttnParams {
   const void *k_new;
   const void *v_new;
   const int64_t *slot_mapping;
-  // Element types: act_f16 = q, k/v rows and out are binary16 (else bf16 on
+  // Element types: act_f32 = everything is fp32; act_f16 = q, k/v rows and out are
+  // binary16 (else bf16 on
   // the step kernel); kv_e4m3 = the caches hold E4M3 codes of K / k_scale and
   // V / v_scale; q16 = the plan kernel's binary16 copy of bf16 queries.
+  int act_f32;
   int act_f16;
   int kv_e4m3;
   float k_scale, v_scale;
@@ -187,8 +189,8 @@ cudaError_t launch_attention_rows(const AttnParams &p, int dtype, cudaStream_t s
 // (attn_chunk_tf32.cu); the decode rows then go to the row kernel (rows_mode 2).
 cudaError_t launch_chunk_tf32(const AttnParams &p, cudaStream_t stream);
 
-// A step of single tokens with 16-bit queries that see a window or selected
-// pages (attn_window_decode.cu),
+// A step of single tokens that see a window (16-bit queries) or selected pages
+// (attn_window_decode.cu),
 // the new rows already in the cache; with rows_mode 2 the single tokens of a
 // mixed step, launched behind the step kernel of its chunks.
 bool window_decode_takes(const AttnParams &p, int sms);

@@ -78,6 +78,35 @@ def test_many_single_tokens_beside_a_chunk(cuda_device, act):
     check(make_batch([1] * 64 + [200], lens, 16, 8, 128, act + "-e4m3", 28, 4, 5, cuda_device))
 
 
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [1, 20, 1]])
+@pytest.mark.parametrize("what,value", [("k", float("nan")), ("k", float("inf")), ("v", float("nan")), ("v", -float("inf")), ("q", float("inf"))])
+def test_fp32_keeps_what_is_not_finite(cuda_device, q_lens, what, value):
+    """One element that the first sequence's row sees: NaN in its outputs (of V: in that dim), nothing elsewhere."""
+    b = make_batch(q_lens, [500, 700, 300], 4, 2, 64, "f32", 6, 2, 17, cuda_device)
+    good = call(b)
+    page = b["table"][0, b["selected"][0, 1, 3]]
+    if what == "q":
+        b["q"][0, 2, 5] = value
+    else:
+        b["k_cache" if what == "k" else "v_cache"][page, 1, 7, 5] = value
+    out = call(b)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    if what == "q":
+        hit[0, 2] = True
+    elif what == "k":
+        hit[0, 2:4] = True
+    else:
+        hit[0, 2:4, 5] = True
+    assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
+
+
+def test_many_fp32_single_tokens(cuda_device):
+    """More rows than are resident at once, and more sequences than the single tokens' kernel takes."""
+    check(make_batch([1] * 90, [40 + 13 * i for i in range(90)], 16, 8, 128, "f32", 5, 1, 18, cuda_device))
+    b = make_batch([1] * 4100, [17 + i % 60 for i in range(4100)], 1, 1, 64, "f32", 2, 1, 19, cuda_device)
+    check(b)
+
+
 def test_large_fp32_steps(cuda_device):
     """Enough tiles for four to a CTA."""
     check(make_batch([700, 1, 90], [1500, 300, 90], 32, 8, 64, "f32", 10, 2, 6, cuda_device))
