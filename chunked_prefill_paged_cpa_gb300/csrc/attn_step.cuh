@@ -73,7 +73,10 @@
 // pages listed for them and their own from page L on, which the position of the
 // first row gives (unit_limit).  The numbering is that of the window with the list in the
 // sinks' place: virtual page v is page list[v], or v + gap behind the list.  The
-// list's length follows from L alone, so the plan needs none of its entries.
+// list's length follows from L alone, so the plan needs none of its entries.  A
+// page that cannot be read (an entry that is no candidate, a column without a page)
+// keeps its place, filled with zeros; the producer raises Bars::skipped, and the
+// softmax warps look for such pages themselves from then on and mask their keys.
 //
 // This header is compiled once per cache mode (attn_step_<mode>.cu), once
 // more with the window (attn_window_<mode>.cu), and with the lists
@@ -168,6 +171,7 @@ struct Bars {
   int bcast[2];
   float red[2][3][4][8];         // [warpgroup][buffer][warp][row]: block maxima, row sums
   float2 mlx[8];                 // decode pipeline 1's (max, sum) per row
+  int skipped;                   // lists: a page of this CTA's items could not be read
   WorkItem items[kItemSlots];
 };
 static_assert(sizeof(Bars) <= 2048, "barrier area overflow");
@@ -214,6 +218,40 @@ template <int G, int VIS>
 __device__ __forceinline__ int pair_kv(const AttnParams &p, int ctx, int q_len, int mp, int mt) {
   const int gap = gap_pages<VIS>(p, ctx - q_len + 2 * mp * (BM / G));
   return tile_kv<G>(ctx - kPage * gap, q_len, min(2 * mp + 1, mt - 1));
+}
+
+// Lists: where the pages of an item stand whose first row is at position x and whose
+// first token is token t0.
+struct Listed {
+  const int32_t *list;  // null in a malformed batch
+  int front, gap;       // pages listed, and left out behind them
+  __device__ __forceinline__ Listed(const AttnParams &p, int x, int t0, int g) {
+    const int limit = unit_limit(p, x);
+    front = min(limit, p.budget);
+    gap = limit - front;
+    list = t0 >= 0 && t0 < p.num_tokens ? p.selected + ((int64_t)t0 * p.Hkv + g) * p.budget : nullptr;
+  }
+  // Block-table column of virtual page v; -1 for an entry that is no candidate.
+  __device__ __forceinline__ int column(int v) const {
+    if (v >= front) return v + gap;
+    const int c = list ? __ldg(list + v) : -1;
+    return c < front + gap ? c : -1;  // (negative entries are none either)
+  }
+};
+
+// Which of the eight pages from virtual page v0 on cannot be read, a lane each.  (A
+// call, as it is hardly ever made: inlined, its registers cost the softmax warps
+// 1 to 4 % of a step.)
+__device__ __noinline__ uint32_t skipped_pages(const Listed at, const int32_t *table, int64_t num_pages,
+                                               int v0, int page_end) {
+  const int lane = threadIdx.x & 31;
+  bool skip = false;
+  if (lane < 8 && v0 + lane < page_end) {
+    const int col = at.column(v0 + lane);
+    const int page = col < 0 ? -1 : __ldg(table + col);
+    skip = page < 0 || page >= num_pages;
+  }
+  return __ballot_sync(0xffffffffu, skip);
 }
 
 // Queue entry written by the plan kernel (32 bytes, two 16-byte stores).
@@ -560,6 +598,14 @@ __device__ __forceinline__ void mask_window(uint32_t (&sr)[32], int n, int a, in
     if (!(keep >> e & 1u)) sr[e] = __float_as_uint(-INFINITY);
 }
 
+// The same over lists, without the two pages' keys whose bit is set.
+__device__ __forceinline__ void mask_pages(uint32_t (&sr)[32], int n, uint32_t pages) {
+  const uint32_t keep = low_bits(n) & ~((pages & 1u) * 0xffffu | (pages >> 1 & 1u) * 0xffff0000u);
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(keep >> e & 1u)) sr[e] = __float_as_uint(-INFINITY);
+}
+
 // p = exp2(s * scale - m) for 32 columns as 16 bf16 (F16: binary16) pairs in
 // `pw`; the fp32 row sum (packed pairs) goes to four independent accumulators.
 template <bool F16>
@@ -796,6 +842,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
     ptx::mbar_init(&bs->mma_done[1], 1);
     ptx::fence_mbar_init();
     bs->mma_lock = 0u;
+    bs->skipped = 0;
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(&bs->tmem_base, 512);
   ptx::tc_fence_before();
@@ -922,32 +969,28 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       // holds page wb + 32 b + l of window b), the next window prefetched
       const int32_t *bt = p.block_table + (int64_t)it.s * p.max_pages;
       const int wb = it.page0 + 8 * it.j0;
-      // virtual pages before the gap: the sinks', or the list of the item's first token
-      int front = VIS == kWindow ? ceil_div(p.sinks, kPage) : 0;
-      const int32_t *listed = nullptr;
-      if (VIS == kSelected) {
-        const int t0 = it.qs + (it.kind == KIND_CHUNK ? 2 * it.mp * TM : 0);
-        const int limit = unit_limit(p, item_first<G>(dsc));
-        front = min(limit, p.budget);
-        if (t0 >= 0 && t0 < p.num_tokens) listed = p.selected + ((int64_t)t0 * p.Hkv + it.g) * p.budget;
-      }
-      auto load_window = [&](int b) -> int {
-        const int pi = wb + 32 * b + lane;
-        if (pi >= it.page_end) return kv_rows;  // past the item: zero fill
-        int col = VIS != kAll && pi >= front ? pi + gap : pi;
-        if (VIS == kSelected && pi < front) {
-          col = listed ? __ldg(listed + pi) : -1;
-          if (col < 0 || col >= front + gap) {
-            atomicOr(p.status, STATUS_BAD_PAGE);
-            return kv_rows;
-          }
-        }
-        const int page = __ldg(bt + col);
+      const int sink_pages = VIS == kWindow ? ceil_div(p.sinks, kPage) : 0;
+      auto place = [&](int col) -> int {
+        const int page = col < 0 ? -1 : __ldg(bt + col);
         if (page < 0 || page >= p.num_pages) {
           atomicOr(p.status, STATUS_BAD_PAGE);
           return kv_rows;
         }
         return (page * p.Hkv + it.g) * kPage;
+      };
+      auto load_window = [&](int b) -> int {
+        const int pi = wb + 32 * b + lane;
+        int row = kv_rows;  // past the item: zero fill
+        if constexpr (VIS == kSelected) {
+          const Listed at(p, item_first<G>(dsc), it.qs + (it.kind == KIND_CHUNK ? 2 * it.mp * TM : 0), it.g);
+          if (pi < it.page_end) row = place(at.column(pi));
+          // (before this lane's arrival at the barrier of any fill with that page)
+          const bool skip = __any_sync(0xffffffffu, pi < it.page_end && row == kv_rows);
+          if (skip && lane == 0) *reinterpret_cast<volatile int *>(&bs->skipped) = 1;
+        } else {
+          if (pi < it.page_end) row = place(VIS != kAll && pi >= sink_pages ? pi + gap : pi);
+        }
+        return row;
       };
       // V lags K by one tile, so the window before the current one is kept too
       int win_prev = kv_rows, win_cur = load_window(0), win_next = load_window(1), win = 0;
@@ -1396,6 +1439,18 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
         }
         return true;
       };
+      // Lists: which of the tile's eight pages from virtual page v0 on were not read.
+      // The flag is looked at behind a tile's S, whose K the producer filled after
+      // it had raised the flag for that tile.  It stays up: the pages are looked up
+      // anew.  (2048 binary16 tokens over 128 pages 90.3 us without this, 91.2 with it;
+      // 512 bf16 tokens over 64 pages 31.0 and 31.6, beside 8 single tokens 37.1 and 36.9.)
+      auto skipped_of = [&](int v0) -> uint32_t {
+        if (!__any_sync(0xffffffffu, *reinterpret_cast<const volatile int *>(&bs->skipped))) return 0u;
+        const bool chunk = it.kind == KIND_CHUNK;
+        const int x = seq_ctx(p, it.s, it.q_len) - it.q_len + (chunk ? 2 * it.mp * TM : 0);
+        const Listed at(p, x, it.qs + (chunk ? 2 * it.mp * TM : 0), it.g);
+        return skipped_pages(at, p.block_table + (int64_t)it.s * p.max_pages, p.num_pages, v0, it.page_end);
+      };
       if (it.kind == KIND_CHUNK) {
         const int q_len = it.q_len;
         const int tok = (2 * it.mp + ti) * TM + r / G;  // index within the chunk
@@ -1414,9 +1469,12 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           // these columns of the tile
           const int wa = VIS == kWindow ? p.sinks - key0 : 0, wb = VIS == kWindow ? last - p.window + 1 - key0 : 0;
           const bool edge = VIS == kWindow && wb > 0 && wa < BN;
+          const uint32_t skip = VIS == kSelected ? skipped_of(key0 / kPage) : 0u;
           auto mask = [&](uint32_t (&x)[32], int c0) {
             if (VIS == kWindow) {
               if (diag || edge) mask_window(x, nvis - c0, wa - c0, wb - c0);
+            } else if (VIS == kSelected) {
+              if (diag || skip) mask_pages(x, nvis - c0, skip >> (c0 / kPage));
             } else if (diag) {
               mask_chunk(x, nvis - c0);
             }
@@ -1628,7 +1686,9 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
           uint32_t sr[G];
           ptx::tmem_ld_cols<G>(tS, sr);
           const int key = (it.page0 + 8 * blk) * kPage + r;
-          const bool valid = key < key_lim && (VIS != kWindow || key < z0 || key >= z1);
+          const uint32_t skip = VIS == kSelected ? skipped_of(it.page0 + 8 * blk) : 0u;
+          const bool valid = key < key_lim && (VIS != kWindow || key < z0 || key >= z1) &&
+                             !(skip >> (r / kPage) & 1u);
           float sv[G];
 #pragma unroll
           for (int q = 0; q < G; ++q) {

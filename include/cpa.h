@@ -423,7 +423,9 @@ int cpa_select_pages(const void *q, const void *summaries, const int32_t *block_
 /* Attention over the selected pages and the last ones.  The lists are those of
  * cpa_select_pages, or any others: their first min(num_selected, L) entries are
  * distinct columns of 0 .. L - 1, in any order; an entry outside is skipped and
- * raises the status word.  num_selected may be 0 (selected is not read).
+ * raises the status word, as does a block_table entry outside [0, num_pages): no
+ * page is read for it, and no key gets its weight.  num_selected may be 0 (selected
+ * is not read).
  * Everything else is as in cpa_window_attention_forward: the whole packed batch,
  * every dtype and cache storage, the workspace, the precision of fp32 steps; the
  * cost is that of the keys that the units see.  Keys and values that no row of a
