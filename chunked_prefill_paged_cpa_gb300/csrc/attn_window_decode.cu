@@ -21,9 +21,11 @@
 // fp32 (KVM 3): m16n8k8 with every operand as two tf32 values (tf32_split.cuh), Q's
 // halves in shared memory, P turned by shuffles.  A page is some 900 instructions,
 // and as keys are the 16 rows of S and dims those of O^T, each element of K and V
-// is split once.  (8 kv heads of 128 with 4 query heads each, 68 pages: 20 / 60
-// tokens 49 / 102 us, 5.1 TB/s; on the kernel of mixed fp32 steps, whose 16 rows a
-// token fills with its 4, 65 / 128 us.)
+// is split once.  A page's products are added up on their own and then, rounded to
+// nearest, to O: the tensor cores cut off towards zero (attn_window_f32.cu).  (8 kv
+// heads of 128 with 4 query heads each, 68 pages: 20 / 60 tokens 51 / 105 us, 5.0
+// TB/s, and 50 / 104 us with the products added to O; on the kernel of mixed fp32
+// steps, whose 16 rows a token fills with its 4, 65 / 128 us.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -355,16 +357,21 @@ __global__ void __launch_bounds__(W * 32) window_decode_kernel(const AttnParams 
         split((r & 1) ? odd : even, ph[j], pl[j]);
       }
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < KS; ++i) {
+        float t[4];
 #pragma unroll
         for (int m = 0; m < 4; m += 2) {
           uint32_t h[4], l[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) split(__uint_as_float(x.v[m + (e >> 1)][2 * i + (e & 1)]), h[e], l[e]);
-          mma_tf32(o[i], h[0], h[1], h[2], h[3], pl[m], pl[m + 1]);
-          mma_tf32(o[i], l[0], l[1], l[2], l[3], ph[m], ph[m + 1]);
-          mma_tf32(o[i], h[0], h[1], h[2], h[3], ph[m], ph[m + 1]);
+          if (m == 0) mma_tf32_first(t, h[0], h[1], h[2], h[3], pl[m], pl[m + 1]);
+          else mma_tf32(t, h[0], h[1], h[2], h[3], pl[m], pl[m + 1]);
+          mma_tf32(t, l[0], l[1], l[2], l[3], ph[m], ph[m + 1]);
+          mma_tf32(t, h[0], h[1], h[2], h[3], ph[m], ph[m + 1]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] += t[e];
+      }
       after_o();
       return;
     }

@@ -39,6 +39,16 @@ namespace {
 constexpr int kPageKeys = 16, kUnitKeys = 8;
 constexpr int kWarps = 4;
 constexpr int kRows = 16;
+// The tensor cores cut what they add up off towards zero: a sum of all of a row's
+// keys in one place loses some 2^-24 with each product, in one direction (2.9e-5 of
+// the output over 4096 keys).  So a sum takes the products of kSumUnits units, and
+// is then added, rounded to nearest, to the one in shared memory: 6.5e-7 over 4096
+// keys, what a plain fp32 product gives.  (4 tokens and a 1000-token chunk, 8 kv heads
+// of 128, window 1024 / 4096: 406 / 1525 us without this, 422 / 1572 with 8 units,
+// 413 / 1540 with 16, which lose 1.0e-6; a new sum for every unit, added in
+// registers, 466 / 1782.  1000 tokens of 2 kv heads of 64 over 64 / 128 pages 75 / 114
+// and 79 / 128 us, the longest loss: less L1 beside the larger shared memory.)
+constexpr int kSumUnits = 8;
 constexpr float kMoveThreshold = 8.0f;  // log2 units, as in the step kernel
 
 // Eight keys of K and V of one kv head as a lane holds them.  With r = lane / 4
@@ -83,8 +93,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int G = p.Hq / p.Hkv, TM = TILES * kRows / G;  // tokens per CTA
-  // Q, split: [tile][k-step][hi, lo][lane], 16 bytes; later the warps' O
+  // Q, split: [tile][k-step][hi, lo][lane], 16 bytes; later the CTA's O.  Then the
+  // warps' O
   extern __shared__ __align__(16) float sm[];
+  float *sm_o = sm + TILES * kRows * D * 2;
 
   // Sequence s owns the CTA numbers from query_start_loc[s] / TM + s on: at
   // least one per TM tokens begun, and some left over.  The last s whose first
@@ -200,6 +212,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   for (int i = 0; i < KS; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  // The sums of the last units are in `o`, at most kSumUnits, and those of the others
+  // in shared memory, in 16-byte words of the lane's own, still to be multiplied by
+  // ka and kb (rows r and r + 8)
+  float4 *kept = reinterpret_cast<float4 *>(sm_o + warp * kRows * D) + lane;
+  bool any_kept = false;
+  float ka = 1.f, kb = 1.f;
+  auto join_kept = [&](bool keep) {
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      if (any_kept) {
+        const float4 y = kept[i * 32];
+        o[i][0] = fmaf(y.x, ka, o[i][0]);
+        o[i][1] = fmaf(y.y, ka, o[i][1]);
+        o[i][2] = fmaf(y.z, kb, o[i][2]);
+        o[i][3] = fmaf(y.w, kb, o[i][3]);
+      }
+      if (keep) {
+        kept[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      }
+    }
+    any_kept = true;
+    ka = kb = 1.f;
+  };
   float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // rows r and r + 8
   const float sl2 = p.scale_log2;
 
@@ -271,6 +308,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
       mb = nb;
       la *= fa;
       lb *= fb;
+      ka *= fa;
+      kb *= fb;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         o[i][0] *= fa;
@@ -301,7 +340,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
     }
     if (u + 1 < u1) x.load_v(vc + at, r, c);
     e = next;
+    if ((u - u0) % kSumUnits == kSumUnits - 1 && u + 1 < u1) join_kept(true);
   }
+  if (any_kept) join_kept(false);
 #pragma unroll
   for (int k = 1; k < 4; k <<= 1) {
     la += __shfl_xor_sync(0xffffffffu, la, k);
@@ -331,9 +372,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   }
   // join the warps, then the cluster's CTAs
   __shared__ float2 sm_ml[kWarps][kRows], cl_ml[kRows];
-  float *sm_o = sm;  // [warp][row][D]
-  float *cl_o = sm + kWarps * kRows * D;
-  __syncthreads();  // Q has been read
+  float *cl_o = sm;  // (sm_o: [warp][row][D])
+  __syncthreads();  // Q and what the lanes kept have been read
   if (c == 0) {
     sm_ml[warp][r] = make_float2(ma, la);
     sm_ml[warp][r + 8] = make_float2(mb, lb);
@@ -384,10 +424,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_f32_kernel(const AttnPa
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-// Q of four tiles; or Q of one tile, later the warps' O and the CTA's.
+// Q of four tiles, or of one, later the CTA's O; and the warps' O.
 template <int D, bool ROWS>
 constexpr int smem_bytes() {
-  return (ROWS ? kWarps * kRows * D * 2 : (kWarps + 1) * kRows * D) * (int)sizeof(float);
+  return ((ROWS ? kWarps : 1) * 2 + kWarps) * kRows * D * (int)sizeof(float);
+}
+
+// Lets the kernel have that much.
+template <int D, bool ROWS, int VIS>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(window_f32_kernel<D, ROWS, VIS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem_bytes<D, ROWS>());
 }
 
 // CTAs resident on an SM of the current device at a time (one tile per CTA).
@@ -396,7 +443,8 @@ int resident() {
   static PerDevice ctas;
   return std::max(1, ctas.get(current_device(), [] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false, VIS>, kWarps * 32,
+    if (allow_smem<D, false, VIS>() != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, window_f32_kernel<D, false, VIS>, kWarps * 32,
                                                       smem_bytes<D, false>()) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -408,8 +456,7 @@ int resident() {
 template <int D, bool ROWS, int VIS>
 cudaError_t launch(const AttnParams &p, int nc, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, ROWS>();
-  const cudaError_t e = cudaFuncSetAttribute(window_f32_kernel<D, ROWS, VIS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<D, ROWS, VIS>();
   if (e != cudaSuccess) return e;
   const int TM = (ROWS ? kWarps : 1) * kRows / (p.Hq / p.Hkv);
   cudaLaunchConfig_t cfg = {};

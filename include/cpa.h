@@ -217,7 +217,8 @@ int cpa_append_attention_forward(const void *q, const void *k, const void *v,
  *    of the group's other rows non-finite, as in cpa_attention_forward.
  *  - fp32 activations keep fp32's precision: the tensor cores multiply each
  *    operand as the sum of two tf32 values, the products' error is below
- *    2^-21 (cpa_attention_forward rounds a chunk's operands to tf32).  There a
+ *    2^-21, and no sum grows for more than 64 keys before it is added up rounded
+ *    to nearest (cpa_attention_forward rounds a chunk's operands to tf32).  There a
  *    non-finite q, K or V that a row sees gives non-finite outputs: NaN
  *    where the formula's value is infinite, and where it is finite because the
  *    key's score is -infinity.  A magnitude of (2 - 2^-11) 2^127 and more, which is
