@@ -415,13 +415,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   const int nu = (tq == 0 || tq >= grid) ? 1 : (int)max(1ll, (long long)kMaxStepGrid / tq);
   const int unit_tiles =
       (int)max((long long)kMinUnitTiles, ((tt + (tp + 7) / 8 + grid - 1) / grid * 3 + 3) / 4);
-  // Over lists all pairs are about as long, and short: split into k units, a pair
+  // Over lists all pairs are about as long: split into k units, eight at most, a pair
   // takes a unit's tiles, and a merge of 3 + k tiles' time, in as many rounds as the
   // units fill the grid; never less than all units' and slices' share.  (2048-key
   // lists, 8 kv heads of 128, binary16; this rule against the one above, us: chunks
   // of 256 / 512 / 768 / 1024 tokens 36 / 42 / 49 / 52 against 36 / 52 / 66 / 78; 512
   // tokens beside 8 / 16 / 32 single tokens of 68 pages, the whole step 63 / 76 / 81
-  // against 72 / 73 / 86.)
+  // against 72 / 73 / 86.  Longer lists: 64 bf16 tokens of 1 / 8 kv heads with 4 query
+  // heads each over 512, 1024, 2048 and 4096 pages 49, 62, 94, 156 / 52, 70, 106, 168 us,
+  // and over a window as long, by the rule above, 46, 69, 94, 147 / 52, 71, 119, 162.)
   auto split = [&](int t) {
     int best = 1, least = INT32_MAX;
     const int slices = (int)min(tp / 12, 1ll << 24);
