@@ -1,15 +1,15 @@
 // Page summaries and the selection of pages by them.
 //
-// A page's summary bounds its keys per kv head: hi_d and lo_d, the largest and the
-// smallest of element d over its 16 keys, as whole numbers of at most 127 times one
-// scale.  For a query q no key of the page has a larger product than
+// Let hi_d and lo_d be the largest and the smallest of element d over a page's 16 keys
+// of a kv head.  For a query q no key of the page has a larger product than
 // sum_d max(q_d hi_d, q_d lo_d); summed over the rows of a unit (the tokens that
 // share a selection, by the heads of the group) that is
 //   sum_d A_d hi_d + B_d lo_d,   A_d = sum_rows max(q_d, 0), B_d = sum_rows min(q_d, 0),
-// one product of 2 D terms per page however many rows the unit has.  The queries
-// are made whole numbers too, and so the sums are exact and their order is free:
-// the selection depends on the inputs alone, and ties, which go to the lower page,
-// are ties everywhere.
+// one product of 2 D terms per page however many rows the unit has.  The score is
+// that with hi and lo, the queries and the sums each rounded to whole numbers of at
+// most 127: an estimate of the bound.  In whole numbers sums are exact and their order
+// is free: the selection depends on the inputs alone, and ties, which go to the lower
+// page, are ties everywhere.
 //
 // Both are bound by HBM: a summary reads 16 keys, a selection reads 1/15 of the
 // keys' bytes of a 16-bit cache.
@@ -397,7 +397,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
 
   // The unit's rows as whole numbers: the largest magnitude, then the sums, then
   // seven bits of each by the same shift.  A short last unit's last token counts for
-  // the tokens that it lacks.
+  // the tokens that it lacks, as the operator is defined; that gives it more than its
+  // share (36 tokens of 4 heads of N(0, 1): 6 to 8 of 32 pages differ from the sum
+  // over the rows).
   constexpr int QL = D / QN;  // 16-byte words of a query; a lane's stand at the same dims
   static_assert(QL <= 32, "a row fits a warp");
   const int rows = tokens << a.log_g;

@@ -402,15 +402,20 @@ int cpa_copy_summaries(const int32_t *src, const int32_t *dst, const int32_t *nu
  * min(num_selected, L) with the highest scores, the lower page where scores are
  * equal, listed in rising order; the list's other entries become -1.
  * The score of a page is scale * (sum_d A[d] hi[d] + B[d] lo[d]), in whole numbers
- * but for one fp32 product with the page's scale; it stands for the sum over the
- * unit's rows (tokens by the G heads) of the largest logit that a key inside the
- * bounds can have.  Of the unit's queries q[r][d], in fp32: a = max |q|,
+ * but for one fp32 product with the page's scale.  It estimates (keys, queries and
+ * sums are rounded: a key's logit may be larger) the sum over the unit's rows, tokens
+ * by the G heads, of the largest logit that a key between the page's extremes can
+ * have.  Of the unit's queries q[r][d], in fp32: a = max |q|,
  * c = round(q * (127 / a)) as above (a < 2^-100, or a query that is not finite: 0),
  * up[d] = sum_r max(c, 0), down[d] = sum_r max(-c, 0) (every unit of a chunk of more
  * than 256 / G tokens counts that many tokens: a short last one its last token once
  * more for each that it lacks), h the least with
  * max(up, down) div 2^h <= 127, A[d] = min(127, (up[d] + 2^h div 2) div 2^h) and
- * -B[d] likewise of down[d].  Pages 0 .. sink_pages - 1 and pages whose scale is
+ * -B[d] likewise of down[d].  So the last token of a short last unit outweighs the
+ * unit's others.  Where each is to count once, describe the unit's tokens as a
+ * sequence of their own on the same pages (the block_table row again; the chunk ends
+ * before them): its lists are those of the sum over its rows, and the attention is
+ * the same.  Pages 0 .. sink_pages - 1 and pages whose scale is
  * +infinity score +infinity; a page whose entry is outside [0, num_pages) comes
  * behind all others and raises the status word.  Every candidate's summary must
  * have been made.  A context of at most num_selected candidates reads none.
