@@ -171,8 +171,8 @@ struct Bars {
   int bcast[2];
   float red[2][3][4][8];         // [warpgroup][buffer][warp][row]: block maxima, row sums
   float2 mlx[8];                 // decode pipeline 1's (max, sum) per row
-  int skipped;                   // lists: a page of this CTA's items could not be read
   WorkItem items[kItemSlots];
+  int skipped;                   // lists: a page of this CTA's items could not be read
 };
 static_assert(sizeof(Bars) <= 2048, "barrier area overflow");
 
@@ -844,7 +844,7 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
     ptx::mbar_init(&bs->mma_done[1], 1);
     ptx::fence_mbar_init();
     bs->mma_lock = 0u;
-    bs->skipped = 0;
+    if (VIS == kSelected) bs->skipped = 0;
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(&bs->tmem_base, 512);
   ptx::tc_fence_before();
@@ -972,27 +972,31 @@ attn_step_kernel(const AttnParams p, const StepWs w, const __grid_constant__ CUt
       const int32_t *bt = p.block_table + (int64_t)it.s * p.max_pages;
       const int wb = it.page0 + 8 * it.j0;
       const int sink_pages = VIS == kWindow ? ceil_div(p.sinks, kPage) : 0;
-      auto place = [&](int col) -> int {
-        const int page = col < 0 ? -1 : __ldg(bt + col);
+      auto load_window = [&](int b) -> int {
+        const int pi = wb + 32 * b + lane;
+        if constexpr (VIS == kSelected) {
+          const Listed at(p, item_first<G>(dsc), it.qs + (it.kind == KIND_CHUNK ? 2 * it.mp * TM : 0), it.g);
+          int page = -1;
+          if (pi < it.page_end) {
+            const int col = at.column(pi);
+            if (col >= 0) page = __ldg(bt + col);
+            if (page < 0 || page >= p.num_pages) {
+              atomicOr(p.status, STATUS_BAD_PAGE);
+              page = -1;
+            }
+          }
+          // (before this lane's arrival at the barrier of any fill with that page)
+          const bool skip = __any_sync(0xffffffffu, pi < it.page_end && page < 0);
+          if (skip && lane == 0) *reinterpret_cast<volatile int *>(&bs->skipped) = 1;
+          return page < 0 ? kv_rows : (page * p.Hkv + it.g) * kPage;
+        }
+        if (pi >= it.page_end) return kv_rows;  // past the item: zero fill
+        const int page = __ldg(bt + (VIS == kWindow && pi >= sink_pages ? pi + gap : pi));
         if (page < 0 || page >= p.num_pages) {
           atomicOr(p.status, STATUS_BAD_PAGE);
           return kv_rows;
         }
         return (page * p.Hkv + it.g) * kPage;
-      };
-      auto load_window = [&](int b) -> int {
-        const int pi = wb + 32 * b + lane;
-        int row = kv_rows;  // past the item: zero fill
-        if constexpr (VIS == kSelected) {
-          const Listed at(p, item_first<G>(dsc), it.qs + (it.kind == KIND_CHUNK ? 2 * it.mp * TM : 0), it.g);
-          if (pi < it.page_end) row = place(at.column(pi));
-          // (before this lane's arrival at the barrier of any fill with that page)
-          const bool skip = __any_sync(0xffffffffu, pi < it.page_end && row == kv_rows);
-          if (skip && lane == 0) *reinterpret_cast<volatile int *>(&bs->skipped) = 1;
-        } else {
-          if (pi < it.page_end) row = place(VIS != kAll && pi >= sink_pages ? pi + gap : pi);
-        }
-        return row;
       };
       // V lags K by one tile, so the window before the current one is kept too
       int win_prev = kv_rows, win_cur = load_window(0), win_next = load_window(1), win = 0;
