@@ -6,7 +6,8 @@
 // rows and the tokens are shared out over the grid.  The operator is bound by a
 // launch and a chain of three dependent loads.  (8 requests 3.0 us; 1024 requests
 // and 19 K tokens of a 2048-column table 7.8 us, four rounds of the sum; with
-// one CTA of 1024 threads on an SM 4.5 and 9.1 us.)
+// one CTA of 1024 threads on an SM 4.5 and 9.1 us.  The grid follows the rows and
+// columns: 32 K tokens of one request are on one CTA, 39 us.)
 #include <algorithm>
 
 #include "cpa_internal.cuh"
