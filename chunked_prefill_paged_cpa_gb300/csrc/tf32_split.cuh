@@ -28,9 +28,9 @@ __device__ __forceinline__ void mma_tf32_first(float (&d)[4], uint32_t a0, uint3
 // its high bits set, the one that fp32 arithmetic here gives among them, that
 // addition would run over into the sign and leave a zero.  So what is not
 // finite, for which x - hi is NaN, keeps its NaN in lo: whatever it is
-// multiplied by is NaN.  (Test and selection cost up to 1 %: 4 tokens and a
-// 1000-token chunk, 8 kv heads of 128, window 1024 / 4096: 415 / 1450 us without,
-// 416 / 1460 with them; both roundings by cvt.rna.tf32, which keeps NaN, 453 / 1568.)
+// multiplied by is NaN.  (Test and selection cost up to 1 %, both roundings by
+// cvt.rna.tf32, which keeps NaN, 8 to 9 %: 4 tokens and a 1000-token chunk, 8 kv heads
+// of 128, window 1024 / 4096, 430 / 1501 us now.)
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   const float rest = x - __uint_as_float(hi);
